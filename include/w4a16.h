@@ -63,8 +63,16 @@ typedef enum {
   W4_OP_LINEAR_G = 4,       /* w4a16_linear_g (zero-points assumed present: an upper bound) */
   W4_OP_GMM_G = 5,          /* moe_w4a16_gmm_g (likewise) */
   W4_OP_LAYER = 6,          /* moe_w4a16_layer: M_or_T = T, N = H, K = I, E, k */
-  W4_OP_LAYER_CTL = 7       /* its control area at the front of that workspace (T ignored) */
+  W4_OP_LAYER_CTL = 7,      /* its control area at the front of that workspace (T ignored) */
+  W4_OP_LINEAR_8 = 8,       /* w4a8_linear */
+  W4_OP_ATTEND = 9          /* kv_cache_attend: M_or_T = B, N = q_heads, K = head_dim, E = kv_heads */
 } w4_op;
+
+typedef enum {
+  W4_KV_BF16 = 0,           /* cache rows in bf16, no scales */
+  W4_KV_INT8 = 1,           /* int8 codes, one bf16 scale per 32 */
+  W4_KV_INT4 = 2            /* int4 codes in layout L1 (nibbles q + 8), one bf16 scale per 32 */
+} w4_kv_kind;
 
 /*
  * w4_repack -- recover int4 codes and bf16 scales from bf16 weights that sit on the Q4_0 grid.
@@ -287,6 +295,109 @@ w4_status moe_rms_chain(const uint16_t* y, int64_t T, int32_t H, float eps, uint
  */
 w4_status w4a16_linear_noalloc(const uint16_t* x, const uint32_t* codes, const uint16_t* scales,
                                uint16_t* y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * w4_rms_add, w4_rms_add_q8 -- residual addition and root-mean-square norm of token rows: the step
+ * in front of a linear or expert layer.  (No counterpart on the pages, which leave out the blocks
+ * between the expert layers; beside moe_rms_chain, with the residual and the weight that a real
+ * decoder layer has, and with the 8-bit rows that w4a8_linear takes.)
+ *
+ *   x          [T, H] bf16.     residual  [T, H] bf16 or NULL.     weight  [H] bf16 or NULL (ones).
+ *   h          [T, H] bf16 (output when residual is given, else untouched): bf16(x + residual).  It
+ *              may be `residual` itself; other outputs may not overlap inputs.
+ *   y          [T, H] bf16: bf16(h_i weight_i / sqrt(mean(h^2) + eps)), with h = x without residual.
+ *   q, q_scale [T, H] int8, [T] float32: the same y, before its rounding to bf16, as
+ *              q_scale = max|y| / 127 per row and q = rint(y / q_scale).  A row of zeros gives scale
+ *              0 and codes 0; a row holding NaN or infinity gives scale NaN and codes 0.
+ *   T >= 0, H % 8 == 0, 8 <= H <= 32768 (W4_ERR_UNSUPPORTED above), eps >= 0.  q 8-byte aligned.
+ * The norm is that of the stored (rounded) h.  The sum of squares is float32 in a fixed order, so
+ * |h| beyond about 2^63 overflows it (y = 0, as in moe_rms_chain); codes can differ from exact
+ * arithmetic by one where y / q_scale is within float32 rounding of a half.
+ */
+w4_status w4_rms_add(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T,
+                     int32_t H, float eps, uint16_t* h, uint16_t* y, void* stream);
+w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T,
+                        int32_t H, float eps, uint16_t* h, int8_t* q, float* q_scale, void* stream);
+
+/*
+ * w4a8_linear -- w4a16_linear on 8-bit activation rows (w4_rms_add_q8's output):
+ *   y[m, n] = bf16(xs[m] * sum_g s[n, g] * sum_{k in group g} xq[m, k] * q[n, k]).
+ * (No counterpart on the pages: an addition of this library, on its weight format.)
+ *
+ *   xq        [M, K] int8.     xs  [M] float32.     codes  [N, K/8] uint32 (layout L1).
+ *   scales    [N, K/32] bf16 (2-byte aligned).      y      [M, N] bf16 (output).
+ *   M >= 0, N >= 1, K >= 32 with K % 32 == 0.
+ *   workspace at least w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1) bytes (may be NULL when that
+ *             is 0).  Its contents need no preparation; calls sharing it must not overlap on the GPU.
+ * Sums inside a group are exact integers; groups are accumulated in float32 in a fixed order.
+ */
+w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
+                      uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * kv_cache_write, kv_cache_read -- rows of a paged key/value cache, quantised as they are written and
+ * read back as bf16.  (No counterpart on the pages; the cache takes the weights' format, symmetric
+ * codes with one bf16 scale per 32.)
+ *
+ *   kind      W4_KV_BF16, W4_KV_INT8 or W4_KV_INT4.
+ *   k_cache, v_cache  [pages, kv_heads, page_size, head_dim] bf16 or int8, or
+ *             [pages, kv_heads, page_size, head_dim / 8] uint32 (layout L1 words); 16-byte aligned.
+ *   k_scales, v_scales  [pages, kv_heads, page_size, head_dim / 32] bf16 (NULL for W4_KV_BF16).
+ *   slots     [T] int64: token t's place, page * page_size + offset.  A negative slot marks a padded
+ *             token: nothing is written for it, and it reads as zeros.  Slots of one write must be
+ *             distinct; a slot named twice holds, byte by byte, either token's row.
+ *   k, v      write: [T, kv_heads, head_dim] bf16 with row strides k_stride, v_stride elements
+ *             (multiples of 8, at least kv_heads * head_dim: columns of a fused projection).
+ *             read: dense outputs [T, kv_heads, head_dim].
+ *   dev_status  one int32 device word or NULL: W4_ERR_INVALID_ARG when a slot lies past the last page
+ *             (that token is treated as padded); left unchanged otherwise.
+ *   head_dim  a multiple of 32, at most 1024; any page_size >= 1.
+ * Per group of 32, with x the bf16 values:  s = bf16(max|x| / top), q = rint(x / s) clamped to
+ * [-top, top], top = 127 (int8) or 7 (int4); a group whose s is 0 holds codes 0; a group holding
+ * NaN or infinity holds codes 0 and a NaN scale (0x7FC0).  Codes and scales are those of exact
+ * arithmetic.  A row stands for s * q; reading rounds that once to bf16.  W4_KV_BF16 copies.
+ */
+w4_status kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                         const int64_t* slots, int64_t T, int32_t kind, int32_t kv_heads, int32_t head_dim,
+                         int64_t pages, int32_t page_size, void* k_cache, void* v_cache, uint16_t* k_scales,
+                         uint16_t* v_scales, int32_t* dev_status, void* stream);
+w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t kv_heads, int32_t head_dim,
+                        int64_t pages, int32_t page_size, const void* k_cache, const void* v_cache,
+                        const uint16_t* k_scales, const uint16_t* v_scales, uint16_t* k, uint16_t* v,
+                        int32_t* dev_status, void* stream);
+
+/*
+ * kv_cache_attend -- attention of one new token per sequence over its cached tokens:
+ *   out[b, h] = sum_t softmax_t(score) * v_t,  score = cap(scale * q[b, h] . k_t),
+ *   cap(z) = softcap * tanh(z / softcap), or z when softcap is 0; the query heads h of
+ *   [g * q_heads / kv_heads, (g + 1) * q_heads / kv_heads) share key/value head g.
+ *
+ *   q          [B, q_heads, head_dim] bf16 with row stride q_stride elements (a multiple of 8).
+ *   k_cache .. kind  as in kv_cache_write; scales 16-byte aligned.
+ *   page_table [B, table_width] int32: pages of each sequence in order.  Entries past a sequence's
+ *              last page are not read.
+ *   seq_lens   [B] int32: cached tokens of each sequence (the new token's row among them, if it has
+ *              been written); 0 gives out = 0 and lse = -infinity.
+ *   window     0, or w > 0: only the last w tokens are seen.
+ *   out        [B, q_heads, head_dim] bf16.    lse  [B, q_heads] float32 or NULL: log sum exp(score).
+ *   workspace  at least w4_workspace_bytes(W4_OP_ATTEND, B, q_heads, head_dim, kv_heads, 0) bytes,
+ *              16-byte aligned; contents need no preparation.  Calls sharing it must not overlap.
+ *   dev_status one int32 device word or NULL: W4_ERR_INVALID_ARG when a length is negative (taken as
+ *              0) or exceeds the table (cut to it), or a page number within the length is outside
+ *              the cache (its tokens are left out); left unchanged otherwise.
+ *   head_dim 64, 128, 192 or 256 (W4_ERR_UNSUPPORTED otherwise); any page_size >= 1;
+ *   q_heads % kv_heads == 0; table_width * page_size < 2^31.
+ * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.
+ * Rows of the cache that no sequence's (windowed) length covers are never looked at.
+ */
+w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                          const uint16_t* k_scales, const uint16_t* v_scales, int32_t kind,
+                          const int32_t* page_table, int32_t table_width, const int32_t* seq_lens,
+                          int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t pages,
+                          int32_t page_size, float scale, float softcap, int32_t window, uint16_t* out,
+                          float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          void* stream);
 
 /* Workspace bytes an entry point needs for the given sizes (0 when it needs none). */
 size_t w4_workspace_bytes(int32_t op, int64_t M_or_T, int64_t N, int64_t K, int32_t E, int32_t k);

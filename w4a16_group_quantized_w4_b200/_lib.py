@@ -28,6 +28,12 @@ W4_OP_LINEAR_G = 4
 W4_OP_GMM_G = 5
 W4_OP_LAYER = 6
 W4_OP_LAYER_CTL = 7
+W4_OP_LINEAR_8 = 8
+W4_OP_ATTEND = 9
+
+W4_KV_BF16 = 0
+W4_KV_INT8 = 1
+W4_KV_INT4 = 2
 
 # name -> (restype, argtypes), mirroring include/w4a16.h
 _P = C.c_void_p
@@ -47,6 +53,14 @@ SIGNATURES = {
     "moe_w4a16_gmm_g": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _P, _I32, _I64, _I32, _I32, _I32, _P,
                                _P, _SZ, _P, _P]),
     "moe_w4a16_layer": (_I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _SZ, _P, _P]),
+    "w4_rms_add": (_I32, [_P, _P, _P, _I64, _I32, C.c_float, _P, _P, _P]),
+    "w4_rms_add_q8": (_I32, [_P, _P, _P, _I64, _I32, C.c_float, _P, _P, _P, _P]),
+    "w4a8_linear": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "kv_cache_write": (_I32, [_P, _P, _I64, _I64, _P, _I64, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P,
+                              _P]),
+    "kv_cache_read": (_I32, [_P, _I64, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "kv_cache_attend": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _I32,
+                               C.c_float, C.c_float, _I32, _P, _P, _P, _SZ, _P, _P]),
     "w4_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32, _I32]),
     "w4_status_str": (C.c_char_p, [_I32]),
     "w4_last_cuda_error": (_I32, []),

@@ -10,6 +10,7 @@ Tensor conventions: bf16 values travel as ``torch.bfloat16`` tensors, packed int
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -371,3 +372,271 @@ class MoELayer:
                       W4_EPI_NONE, out=self.o, stream=stream)
         moe_combine(self.o, self.rt.topk_w, self.rt.pair_pos, y=self.y, stream=stream)
         return self.y
+
+
+# ---------------------------------------------------------------------------------------------
+# the steps around the expert layers: norm, 8-bit linear, key/value cache and its attention
+# ---------------------------------------------------------------------------------------------
+
+def _device_call(fn):
+    """Runs fn with the current device and stream set as its arguments ask: on `stream` when one is
+    given (allocations included, so that a returned tensor belongs to that stream), otherwise on
+    the current stream of the first tensor's device, whichever device is current."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor):
+            raise TypeError(f"{fn.__name__}: expected a torch.Tensor first")
+        if not first.is_cuda:
+            raise ValueError(f"{fn.__name__}: tensors must live on a CUDA device")
+        dev = first.device
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream: expected device {dev}, got {stream.device}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _cur(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows3(name, t, heads, dim, dev):
+    """A bf16 [T, heads, dim] tensor whose rows may be columns of a wider one; its row stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected shape [rows, {heads}, {dim}], got {tuple(t.shape)}")
+    s = t.stride()
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{name}: heads and elements of a row must be contiguous")
+    return s[0] if t.shape[0] > 1 else heads * dim
+
+
+def _scratch(nbytes: int, dev):
+    """Scratch for one call, from torch's stream-ordered allocator: calls on different streams never
+    share it, and a call captured into a CUDA graph keeps it in that graph's own pool."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _rms_args(x, residual, weight, h):
+    if x.dim() != 2:
+        raise ValueError("x: expected two dimensions")
+    T, H = x.shape
+    dev = x.device
+    _need("x", x, torch.bfloat16)
+    if residual is not None:
+        _need("residual", residual, torch.bfloat16, (T, H), dev)
+        h = torch.empty_like(x) if h is None else h
+        _need("h", h, torch.bfloat16, (T, H), dev)
+    elif h is not None:
+        raise ValueError("h: only written when a residual is given")
+    if weight is not None:
+        _need("weight", weight, torch.bfloat16, (H,), dev)
+    return T, H, dev, h
+
+
+@_device_call
+def w4_rms_add(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, y=None):
+    """h = bf16(x + residual), y = bf16(h * weight / sqrt(mean over each row of h^2 + eps)); bf16
+    [T, H] -> (y, h).  h is x itself without a residual; h may be passed as the residual's own
+    buffer to update it in place."""
+    T, H, dev, h = _rms_args(x, residual, weight, h)
+    y = torch.empty_like(x) if y is None else y
+    _need("y", y, torch.bfloat16, (T, H), dev)
+    _lib.check("w4_rms_add", _lib.load().w4_rms_add(
+        x.data_ptr(), _ptr(residual), _ptr(weight), T, H, eps, _ptr(h), y.data_ptr(), _cur(dev)))
+    return y, x if h is None else h
+
+
+@_device_call
+def w4_rms_add_q8(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, q=None, q_scale=None):
+    """w4_rms_add with 8-bit rows: (q int8 [T, H], q_scale f32 [T], h), y = q_scale * q."""
+    T, H, dev, h = _rms_args(x, residual, weight, h)
+    q = torch.empty((T, H), dtype=torch.int8, device=dev) if q is None else q
+    q_scale = torch.empty(T, dtype=torch.float32, device=dev) if q_scale is None else q_scale
+    _need("q", q, torch.int8, (T, H), dev)
+    _need("q_scale", q_scale, torch.float32, (T,), dev)
+    _lib.check("w4_rms_add_q8", _lib.load().w4_rms_add_q8(
+        x.data_ptr(), _ptr(residual), _ptr(weight), T, H, eps, _ptr(h), q.data_ptr(), q_scale.data_ptr(), _cur(dev)))
+    return q, q_scale, x if h is None else h
+
+
+@_device_call
+def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
+    """y [M, N] = xs * (xq [M, K] int8 @ dequant(codes, scales)^T), bf16 out."""
+    lib = _lib.load()
+    if xq.dim() != 2 or codes.dim() != 2:
+        raise ValueError("xq, codes: expected two dimensions")
+    M, K = xq.shape
+    N = codes.shape[0]
+    dev = xq.device
+    _need("xq", xq, torch.int8)
+    _need("xs", xs, torch.float32, (M,), dev)
+    _need("codes", codes, torch.int32, (N, K // 8), dev)
+    _need("scales", scales, torch.bfloat16, (N, K // 32), dev)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    _need("y", y, torch.bfloat16, (M, N), dev)
+    if ws is None:
+        ws = _scratch(lib.w4_workspace_bytes(_lib.W4_OP_LINEAR_8, M, N, K, 1, 1), dev)
+    else:
+        _need("ws", ws, torch.uint8, None, dev)
+    _lib.check("w4a8_linear", lib.w4a8_linear(
+        xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K,
+        _ptr(ws), 0 if ws is None else ws.numel(), _cur(dev)))
+    return y
+
+
+_KV_KINDS = {torch.bfloat16: (_lib.W4_KV_BF16, 1), torch.int8: (_lib.W4_KV_INT8, 1), torch.int32: (_lib.W4_KV_INT4, 8)}
+
+
+def _cache_args(k_cache, v_cache, k_scales, v_scales, dev):
+    """(kind, kv_heads, head_dim, pages, page_size) of a cache, its tensors checked."""
+    if k_cache.dtype not in _KV_KINDS:
+        raise TypeError(f"k_cache: expected bfloat16, int8 or int32 words, got {k_cache.dtype}")
+    kind, per = _KV_KINDS[k_cache.dtype]
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: expected [pages, kv_heads, page_size, head_dim]")
+    _need("k_cache", k_cache, k_cache.dtype, None, dev)
+    _need("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
+    pages, heads, page_size, dim = k_cache.shape
+    dim *= per
+    if kind == _lib.W4_KV_BF16:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales, v_scales: a bfloat16 cache has none")
+    else:
+        want = (pages, heads, page_size, dim // 32)
+        _need("k_scales", k_scales, torch.bfloat16, want, dev)
+        _need("v_scales", v_scales, torch.bfloat16, want, dev)
+    return kind, heads, dim, pages, page_size
+
+
+@_device_call
+def kv_cache_write(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None, dev_status=None):
+    """Rows k, v bf16 [T, kv_heads, head_dim] (rows may be strided) into the cache's slots int64 [T]
+    (page * page_size + offset, negative: padded), quantised to the cache's kind: bfloat16, int8,
+    or int4 (int32 words)."""
+    dev = k.device
+    kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
+    T = k.shape[0]
+    ks, vs = _rows3("k", k, heads, dim, dev), _rows3("v", v, heads, dim, dev)
+    if v.shape[0] != T:
+        raise ValueError(f"v: expected {T} rows, got {v.shape[0]}")
+    _need("slots", slots, torch.int64, (T,), dev)
+    if dev_status is not None:
+        _need("dev_status", dev_status, torch.int32, (1,), dev)
+    _lib.check("kv_cache_write", _lib.load().kv_cache_write(
+        k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, kind, heads, dim, pages, page_size,
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _ptr(dev_status), _cur(dev)))
+
+
+@_device_call
+def kv_cache_read(slots, k_cache, v_cache, k_scales=None, v_scales=None, k=None, v=None, dev_status=None):
+    """The rows of slots int64 [T] as (k, v) bf16 [T, kv_heads, head_dim]; zeros for negative slots."""
+    dev = slots.device
+    kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
+    T = slots.shape[0]
+    _need("slots", slots, torch.int64, (T,), dev)
+    k = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev) if v is None else v
+    _need("k", k, torch.bfloat16, (T, heads, dim), dev)
+    _need("v", v, torch.bfloat16, (T, heads, dim), dev)
+    if dev_status is not None:
+        _need("dev_status", dev_status, torch.int32, (1,), dev)
+    _lib.check("kv_cache_read", _lib.load().kv_cache_read(
+        slots.data_ptr(), T, kind, heads, dim, pages, page_size, k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(k_scales), _ptr(v_scales), k.data_ptr(), v.data_ptr(), _ptr(dev_status), _cur(dev)))
+    return k, v
+
+
+@_device_call
+def kv_cache_attend(q, k_cache, v_cache, page_table, seq_lens, k_scales=None, v_scales=None, scale=None,
+                    softcap: float = 0.0, window: int = 0, out=None, lse=None, ws=None, dev_status=None):
+    """Attention of one query row per sequence, q bf16 [B, q_heads, head_dim] (rows may be strided),
+    over the cached tokens named by page_table int32 [B, width] and seq_lens int32 [B] -> out bf16
+    [B, q_heads, head_dim].  scale: 1 / sqrt(head_dim) when None; softcap, window: 0 for none;
+    lse: float32 [B, q_heads] to receive log sum exp(score)."""
+    lib = _lib.load()
+    dev = q.device
+    kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
+    if q.dim() != 3:
+        raise ValueError("q: expected [B, q_heads, head_dim]")
+    B, q_heads, _ = q.shape
+    qs = _rows3("q", q, q_heads, dim, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected [B, width]")
+    width = page_table.shape[1]
+    _need("page_table", page_table, torch.int32, (B, width), dev)
+    _need("seq_lens", seq_lens, torch.int32, (B,), dev)
+    out = torch.empty((B, q_heads, dim), dtype=torch.bfloat16, device=dev) if out is None else out
+    _need("out", out, torch.bfloat16, (B, q_heads, dim), dev)
+    if lse is not None:
+        _need("lse", lse, torch.float32, (B, q_heads), dev)
+    if dev_status is not None:
+        _need("dev_status", dev_status, torch.int32, (1,), dev)
+    if ws is None:
+        ws = _scratch(lib.w4_workspace_bytes(_lib.W4_OP_ATTEND, B, q_heads, dim, heads, 0), dev)
+    else:
+        _need("ws", ws, torch.uint8, None, dev)
+    _lib.check("kv_cache_attend", lib.kv_cache_attend(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind,
+        page_table.data_ptr(), width, seq_lens.data_ptr(), B, q_heads, heads, dim, pages, page_size,
+        dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel(), _ptr(dev_status), _cur(dev)))
+    return out
+
+
+class KVCache:
+    """One layer's paged key/value cache and the calls on it.  kind: "bf16", "int8" or "int4" (codes
+    with one bf16 scale per 32 elements of head_dim).  Freshly made it is zero throughout."""
+
+    def __init__(self, pages: int, kv_heads: int, page_size: int, head_dim: int, kind: str = "int8", device="cuda"):
+        if kind not in ("bf16", "int8", "int4"):
+            raise ValueError(f"kind: expected bf16, int8 or int4, got {kind}")
+        if head_dim % 32:
+            raise ValueError("head_dim: expected a multiple of 32")
+        dtype, per = {"bf16": (torch.bfloat16, 1), "int8": (torch.int8, 1), "int4": (torch.int32, 8)}[kind]
+        shape = (pages, kv_heads, page_size)
+        # int4 codes are stored as q + 8
+        fill = -0x77777778 if kind == "int4" else 0
+        self.k = torch.full((*shape, head_dim // per), fill, dtype=dtype, device=device)
+        self.v = torch.full((*shape, head_dim // per), fill, dtype=dtype, device=device)
+        self.k_scales = self.v_scales = None
+        if kind != "bf16":
+            self.k_scales = torch.zeros((*shape, head_dim // 32), dtype=torch.bfloat16, device=device)
+            self.v_scales = torch.zeros_like(self.k_scales)
+        self.kind, self.page_size = kind, page_size
+
+    def write(self, k, v, slots, **kw):
+        """kv_cache_write into this cache."""
+        kv_cache_write(k, v, slots, self.k, self.v, self.k_scales, self.v_scales, **kw)
+
+    def read(self, slots, **kw):
+        """kv_cache_read from this cache."""
+        return kv_cache_read(slots, self.k, self.v, self.k_scales, self.v_scales, **kw)
+
+    def attend(self, q, page_table, seq_lens, **kw):
+        """kv_cache_attend over this cache."""
+        return kv_cache_attend(q, self.k, self.v, page_table, seq_lens, self.k_scales, self.v_scales, **kw)
+
+    def slots(self, page_table, positions):
+        """Slots int64 [B] of one position per sequence (int tensor [B]; negative positions stay
+        padded): where a decode step writes its new rows."""
+        pos = positions.long()
+        at = pos.clamp(min=0)
+        page = torch.gather(page_table.long(), 1, (at // self.page_size)[:, None])[:, 0]
+        return torch.where(pos < 0, -torch.ones_like(pos), page * self.page_size + at % self.page_size)
+
+    def nbytes(self) -> int:
+        """Device bytes of codes and scales."""
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scales, self.v_scales) if t is not None)

@@ -31,6 +31,9 @@ w4_status w4_launch_combine(const uint16_t* o, const float* topk_w, const int32_
                             int k, int H, uint16_t* y, cudaStream_t stream);
 w4_status w4_launch_rms_chain(const uint16_t* y, int64_t T, int H, float eps, uint16_t* x,
                               cudaStream_t stream, int sm_count);
+// workspaces of the entry points that live beside their kernels (w4a8.cu, kv_attend.cu)
+size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t w4_attend_workspace_bytes(int64_t B, int64_t q_heads, int64_t head_dim, int64_t kv_heads);
 size_t w4_stream_workspace_bytes(int64_t rows, int N, int K, int E, int epi, bool dense, int sm_count,
                                  bool zp = false);
 w4_status w4_launch_stream_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int k_div,
@@ -159,6 +162,10 @@ size_t w4_workspace_bytes(int32_t op, int64_t M_or_T, int64_t N, int64_t K, int3
         return w4_layer_workspace_bytes(static_cast<int>(M_or_T), E, k, static_cast<int>(N), static_cast<int>(K),
                                         current_sm_count());
       return w4_layer_control_bytes(E, k, static_cast<int>(N), static_cast<int>(K), current_sm_count());
+    case W4_OP_LINEAR_8:
+      return w4_linear8_workspace_bytes(M_or_T, N, K);
+    case W4_OP_ATTEND:
+      return w4_attend_workspace_bytes(M_or_T, N, K, E);
     default:
       return 0;
   }

@@ -1,0 +1,180 @@
+// w4_rms_add, w4_rms_add_q8: residual addition and root-mean-square norm of token rows, in bf16 or
+// as 8-bit codes with one float32 scale per row.
+//
+// Per row, h = bf16(x + residual) is stored and normalised:
+//   y_i = (h_i * w_i) * (1 / sqrt(mean(h^2) + eps)).
+// h_i * w_i is exact in float32 (two 8-bit significands), and multiplication by one positive
+// number keeps the order, so max|y| = max|h w| * (1 / rms): both row statistics come out of one
+// pass over registers and one reduction, and every input byte is read once.  The 8-bit form takes
+// s = max|y| / 127 and q_i = rint(y_i / s).
+//
+// Bound by memory: x, residual and h at 2 bytes an element, y at 2 or 1.  A row is held in the
+// registers of 1 to 32 warps, CPT 16-byte chunks a thread; short rows share a block, so that a
+// block has at least 3 warps.
+#include "common.cuh"
+#include "entry.cuh"
+
+namespace w4 {
+namespace ra {
+
+// wpr warps per row, blockDim.x / (32 wpr) rows per block.
+template <int CPT, bool Q8>
+__global__ void __launch_bounds__(1024)
+rms_add_kernel(const uint16_t* __restrict__ x, const uint16_t* residual, const uint16_t* __restrict__ weight,
+               int64_t T, int H, float eps, int wpr, uint16_t* h_out, uint16_t* __restrict__ y,
+               int8_t* __restrict__ q, float* __restrict__ q_scale) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_in_block = warp / wpr;
+  const int rpb = (blockDim.x >> 5) / wpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + row_in_block;
+  const int tid = threadIdx.x - row_in_block * wpr * 32;   // thread within the row
+  const int tpr = wpr * 32;
+  const int nv = H >> 3;                                   // 16-byte chunks
+  const bool live = row < T;
+  const uint4* xr = reinterpret_cast<const uint4*>(x + row * H);
+  const uint4* rr = residual ? reinterpret_cast<const uint4*>(residual + row * H) : nullptr;
+
+  uint4 hv[CPT], rv[CPT];
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    const int i = c * tpr + tid;
+    const bool ok = live && i < nv;
+    hv[c] = ok ? __ldg(xr + i) : make_uint4(0, 0, 0, 0);
+    // plain load: h_out may be residual itself
+    if (residual) rv[c] = ok ? rr[i] : make_uint4(0, 0, 0, 0);
+  }
+  float sum = 0.f;
+  uint32_t amax = 0;                                       // largest |h w| as a bit pattern: NaN > inf > finite
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    const int i = c * tpr + tid;
+    if (!(live && i < nv)) continue;
+    uint32_t* hw = reinterpret_cast<uint32_t*>(&hv[c]);
+    if (residual) {
+      const uint32_t* rw = reinterpret_cast<const uint32_t*>(&rv[c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        hw[j] = pack_bf16x2(bf16_lo_to_f32(hw[j]) + bf16_lo_to_f32(rw[j]), bf16_hi_to_f32(hw[j]) + bf16_hi_to_f32(rw[j]));
+      reinterpret_cast<uint4*>(h_out + row * H)[i] = hv[c];
+    }
+    uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (Q8 && weight) wv = __ldg(reinterpret_cast<const uint4*>(weight) + i);
+    const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = bf16_lo_to_f32(hw[j]), b = bf16_hi_to_f32(hw[j]);
+      sum = fmaf(a, a, sum);
+      sum = fmaf(b, b, sum);
+      if (Q8) {
+        amax = max(amax, __float_as_uint(a * bf16_lo_to_f32(ww[j])) & 0x7FFFFFFFu);
+        amax = max(amax, __float_as_uint(b * bf16_hi_to_f32(ww[j])) & 0x7FFFFFFFu);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (Q8) amax = __reduce_max_sync(0xffffffffu, amax);
+  if (wpr > 1) {
+    if (lane == 0) { s_sum[warp] = sum; s_max[warp] = amax; }
+    __syncthreads();
+    sum = 0.f;
+    amax = 0;
+    for (int w = 0; w < wpr; ++w) {
+      sum += s_sum[row_in_block * wpr + w];
+      if (Q8) amax = max(amax, s_max[row_in_block * wpr + w]);
+    }
+  }
+  if (!live) return;
+  const float inv = 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
+  float s = 0.f;
+  bool finite = true;
+  if (Q8) {
+    // a row holding NaN or infinity: scale NaN, codes 0, so that it stands for NaN throughout
+    finite = amax < 0x7F800000u && sum < __int_as_float(0x7F800000);
+    s = finite ? __uint_as_float(amax) * inv / 127.f : __int_as_float(0x7FC00000);
+    if (tid == 0) q_scale[row] = s;
+  }
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    const int i = c * tpr + tid;
+    if (i >= nv) break;
+    uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (weight) wv = __ldg(reinterpret_cast<const uint4*>(weight) + i);
+    const uint32_t* ww = reinterpret_cast<const uint32_t*>(&wv);
+    const uint32_t* hw = reinterpret_cast<const uint32_t*>(&hv[c]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo_to_f32(hw[j]) * bf16_lo_to_f32(ww[j]) * inv;
+      v[2 * j + 1] = bf16_hi_to_f32(hw[j]) * bf16_hi_to_f32(ww[j]) * inv;
+    }
+    if (Q8) {
+      uint32_t o[2] = {0, 0};
+      if (finite && s > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int code = max(-127, min(127, __float2int_rn(__fdiv_rn(v[j], s))));
+          o[j >> 2] |= static_cast<uint32_t>(code & 0xFF) << (8 * (j & 3));
+        }
+      }
+      reinterpret_cast<uint2*>(q + row * H)[i] = make_uint2(o[0], o[1]);
+    } else {
+      reinterpret_cast<uint4*>(y + row * H)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+  }
+}
+
+template <int CPT, bool Q8>
+void launch_cpt(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int H, float eps,
+                uint16_t* h, uint16_t* y, int8_t* q, float* qs, cudaStream_t stream) {
+  const int nv = H / 8;
+  const int wpr = (nv + 32 * CPT - 1) / (32 * CPT);        // at most 32: the caller picked CPT
+  const int rpb = wpr >= 4 ? 1 : 4 / wpr;
+  const int64_t grid = (T + rpb - 1) / rpb;
+  rms_add_kernel<CPT, Q8><<<static_cast<unsigned>(grid), 32 * wpr * rpb, 0, stream>>>(x, residual, weight, T, H, eps,
+                                                                                     wpr, h, y, q, qs);
+}
+
+constexpr int kMaxH = 8 * 4 * 1024;                        // CPT 4, 1024 threads
+
+template <bool Q8>
+w4_status run(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int32_t H, float eps,
+              uint16_t* h, uint16_t* y, int8_t* q, float* qs, void* stream) {
+  if (T < 0 || H < 8 || H % 8 || !(eps >= 0.f) || eps > 1e30f) return W4_ERR_INVALID_ARG;
+  if (H > kMaxH || T > 0x7FFFFFFFLL) return W4_ERR_UNSUPPORTED;
+  if (T == 0) return W4_OK;
+  if (!x || (residual && !h) || (Q8 ? (!q || !qs) : !y)) return W4_ERR_INVALID_ARG;
+  if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(weight, 16) || !aligned_to(h, 16) ||
+      !aligned_to(y, 16) || !aligned_to(q, 8) || !aligned_to(qs, 4))
+    return W4_ERR_INVALID_ARG;
+  auto s = static_cast<cudaStream_t>(stream);
+  const int nv = H / 8;
+  // few rows: one chunk a thread for the shortest chain; many rows: more bytes in flight a thread
+  const int64_t few = 2 * device_sm_count();
+  if (nv <= 1024 && T <= few) launch_cpt<1, Q8>(x, residual, weight, T, H, eps, h, y, q, qs, s);
+  else if (nv <= 2048) launch_cpt<2, Q8>(x, residual, weight, T, H, eps, h, y, q, qs, s);
+  else launch_cpt<4, Q8>(x, residual, weight, T, H, eps, h, y, q, qs, s);
+  return launched();
+}
+
+}  // namespace ra
+}  // namespace w4
+
+extern "C" {
+
+w4_status w4_rms_add(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int32_t H,
+                     float eps, uint16_t* h, uint16_t* y, void* stream) {
+  const w4::EntryRange range("w4_rms_add");
+  return w4::ra::run<false>(x, residual, weight, T, H, eps, h, y, nullptr, nullptr, stream);
+}
+
+w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int32_t H,
+                        float eps, uint16_t* h, int8_t* q, float* q_scale, void* stream) {
+  const w4::EntryRange range("w4_rms_add_q8");
+  return w4::ra::run<true>(x, residual, weight, T, H, eps, h, nullptr, q, q_scale, stream);
+}
+
+}  // extern "C"

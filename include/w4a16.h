@@ -387,7 +387,8 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  *              0) or exceeds the table (cut to it), or a page number within the length is outside
  *              the cache (its tokens are left out); left unchanged otherwise.
  *   head_dim 64, 128, 192 or 256 (W4_ERR_UNSUPPORTED otherwise); any page_size >= 1;
- *   q_heads % kv_heads == 0; table_width * page_size < 2^31.
+ *   q_heads % kv_heads == 0; table_width * page_size < 2^31 - 4096 and, times q_heads, below
+ *   2^36; pages * kv_heads * page_size < 2^32 (W4_ERR_UNSUPPORTED beyond).
  * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.
  * Rows of the cache that no sequence's (windowed) length covers are never looked at.
  */

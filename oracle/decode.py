@@ -87,16 +87,16 @@ def row_values(q, s):
 # ------------------------------------------------------------------------------- attention
 def attend(q, k, v, scale, softcap=0.0, window=0):
     """One query row over one sequence's tokens: q [D], k, v [L, D] float64
-    -> (out [D], lse, magnitude sum p |v|, largest sum |q k|)."""
+    -> (out [D], lse, magnitude sum p |v|, largest sum |q k|, sum |v|)."""
     L = k.shape[0]
     if window:
         k, v = k[max(0, L - window):], v[max(0, L - window):]
     if k.shape[0] == 0:
-        return np.zeros(q.shape[0]), -np.inf, np.zeros(q.shape[0]), 0.0
+        return np.zeros(q.shape[0]), -np.inf, np.zeros(q.shape[0]), 0.0, np.zeros(q.shape[0])
     z = (k @ q) * scale
     if softcap:
         z = softcap * np.tanh(z / softcap)
     top = z.max()
     e = np.exp(z - top)
     p = e / e.sum()
-    return p @ v, top + np.log(e.sum()), p @ np.abs(v), float((np.abs(k) @ np.abs(q)).max())
+    return p @ v, top + np.log(e.sum()), p @ np.abs(v), float((np.abs(k) @ np.abs(q)).max()), np.abs(v).sum(axis=0)

@@ -43,10 +43,10 @@ def test_attention_of_two_tokens():
     q = np.array([1.0, 0.0])
     k = np.array([[0.0, 5.0], [np.log(3.0), 0.0]])
     v = np.array([[4.0, 0.0], [0.0, 8.0]])
-    out, lse, _, _ = decode.attend(q, k, v, 1.0)
+    out, lse, *_ = decode.attend(q, k, v, 1.0)
     assert np.allclose(out, [1.0, 6.0]) and np.isclose(lse, np.log(4.0))
     assert np.allclose(decode.attend(q, k, v, 1.0, window=1)[0], v[1])
-    out, lse, _, _ = decode.attend(q, k[:0], v[:0], 1.0)
+    out, lse, *_ = decode.attend(q, k[:0], v[:0], 1.0)
     assert not out.any() and lse == -np.inf
     assert np.isclose(decode.attend(q, k, v, 1.0, softcap=0.5)[1],
                       np.log(1 + np.exp(0.5 * np.tanh(2 * np.log(3.0)))))

@@ -1,0 +1,815 @@
+// The attention kernel of kv_cache_attend (instantiated per cache kind in kv_attend_*.cu).
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(z_t - m),  z_t = log2(e) * cap(scale * q . k_t)
+//
+// One pass over the cache with a running reference m per head.  Bound by the cache's bytes, each of
+// which is needed once, so nothing is staged in shared memory: the tensor-core operands are loaded
+// straight from global memory into the registers of the lanes that feed them.
+//   * Scores, S^T = K Q^T: tokens are the 16 rows of an m16n8k16 product, up to 8 query heads of one
+//     key/value head its 8 columns.  The product does not care in which order the head dimension
+//     is summed, so lane (r, t) = (lane / 4, lane % 4) takes the 8 consecutive elements 32 g + 8 t of
+//     token rows r and r + 8: a quad reads 64 (bf16), 32 (int8) or 16 (int4) contiguous bytes a row.
+//   * Outputs, O^T = V^T P^T: head-dimension elements are the 16 rows, tokens the 16 summed ones.  Lane
+//     (r, t) loads VE consecutive elements at VE r of tokens 2t, 2t+1, 2t+8, 2t+9 (eight lanes read
+//     whole 128-byte lines where a row has them) and byte permutes pair the tokens up.
+//   * The weights p leave the first product with tokens along r and enter the second with tokens
+//     along t: one 8x8 register transpose (movmatrix) per 8 tokens.
+// Codes are widened to fp16 exactly.  Key scales multiply the float32 sum of their group; value
+// scales multiply the widened code in fp16, brought into range by a power of two per output row
+// (one more rounding of 2^-11; scaling the weights instead would need a weight per group).  Weights are
+// rounded to fp16 against quantised values; against bf16 values they enter as a bf16 pair (high and
+// remainder, two products), because a single bf16 would cost as much as the output's own rounding.
+//
+// Work is cut over all lengths: sequences' (windowed) tokens in units of 64, times key/value heads
+// times blocks of 8 query heads, form one line that the blocks of the grid share evenly.  A block that
+// holds an item (sequence, heads) whole writes its output; parts go to the workspace and a second
+// kernel joins them in order.
+#pragma once
+
+#include "common.cuh"
+#include "entry.cuh"
+
+namespace w4 {
+namespace at {
+
+constexpr int kUnit = 64;             // tokens a work unit
+constexpr int kWarps = 4;
+constexpr int kHeads = 8;             // query heads an item
+constexpr int64_t kMostTokens = 0x7FFFEFFF;   // a sequence's table: token numbers stay below 2^31 past its end
+constexpr float kLowest = -3.0e38f;   // reference before any token: finite, so that masked scores give p = 0
+constexpr float kSlack = 8.f;         // a reference is raised once a score passes it by 2^kSlack
+constexpr float kLift = 6.f;          // weights for fp16 are taken times 2^kLift: at most 2^14
+
+struct Args {
+  const uint16_t* q;
+  int64_t q_stride;
+  const void *k, *v;
+  const uint16_t *ks, *vs;
+  const int32_t *table, *lens;
+  int table_width, B, q_heads, kv_heads, page_size;
+  int pages;
+  float scale, softcap;
+  int window;
+  uint16_t* out;
+  float* lse;
+  float* parts;                       // [2 * grid][kHeads * (D + 2)]: sums, references, totals
+  int32_t* dev_status;
+  // derived
+  int G, HB;                          // query heads per key/value head, blocks of 8 of them
+};
+
+// A sequence's visible tokens [first, len) and the units that cover them.
+struct Span {
+  int first, len, u0, n;
+};
+__device__ __forceinline__ Span span_of(const Args& a, int b, bool report) {
+  Span s;
+  int len = __ldg(a.lens + b);
+  const int most = a.table_width * a.page_size;
+  if (len < 0 || len > most) {
+    if (report) set_status(a.dev_status, W4_ERR_INVALID_ARG);
+    len = len < 0 ? 0 : most;
+  }
+  s.len = len;
+  s.first = a.window > 0 && len > a.window ? len - a.window : 0;
+  s.u0 = s.first / kUnit;
+  s.n = len > 0 ? (len + kUnit - 1) / kUnit - s.u0 : 0;
+  return s;
+}
+
+template <int KIND, int D>
+struct Cfg {
+  static constexpr int KW = KIND == W4_KV_BF16 ? 4 : KIND == W4_KV_INT8 ? 2 : 1;   // words per 8 elements
+  static constexpr int ROWW = D / 8 * KW;                                           // words per row
+  static constexpr int NG = D / 32;                                                 // groups per row
+  static constexpr int VE = KIND == W4_KV_BF16 ? 8
+                            : KIND == W4_KV_INT8 ? (D % 128 == 0 ? 16 : 8)
+                            : (D % 256 == 0 ? 32 : D % 128 == 0 ? 16 : 8);
+  static constexpr int VW = VE / 8 * KW;
+  static constexpr int NV = D / (8 * VE);
+  // 16-token tiles a warp takes at once: about 4 KB of keys and as much of values in flight
+  static constexpr int TT = KIND == W4_KV_BF16 ? (D == 64 ? 2 : 1)
+                            : KIND == W4_KV_INT8 ? (D == 64 ? 4 : D == 128 ? 2 : 1)
+                            : (D == 64 ? 4 : D == 128 ? 4 : D == 192 ? 2 : 2);
+  static constexpr int MINB = D == 64 ? 4 : D == 128 ? 3 : 2;                       // blocks per SM
+};
+
+template <int W>
+__device__ __forceinline__ void ldg_words(uint32_t (&o)[W], const uint32_t* p) {
+  if constexpr (W == 4) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    o[0] = v.x; o[1] = v.y;
+  } else {
+    o[0] = __ldg(p);
+  }
+}
+
+// NG bf16 scales of a row as (NG + 1) / 2 words
+template <int NG>
+__device__ __forceinline__ void ldg_scales(uint32_t (&o)[NG / 2], const uint16_t* p) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+  if constexpr (NG == 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w));
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  } else if constexpr (NG == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(w));
+    o[0] = v.x; o[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) o[i] = __ldg(w + i);
+  }
+}
+
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// bytes (already offset by 128) 0, 1 or 2, 3 of v -> fp16 pair of the signed values, exactly:
+// 0x6400 | u is 1024 + u
+template <int SEL>
+__device__ __forceinline__ uint32_t bytes_h2(uint32_t v) {
+  return h2_add(__byte_perm(v, 0x64646464u, SEL), 0xE480E480u);        // - 1152
+}
+__device__ __forceinline__ uint32_t nib_lo_h2(uint32_t v) { return h2_add(nib_f16x2_lo(v), 0xE408E408u); }   // - 1032
+__device__ __forceinline__ uint32_t nib_hi_h2(uint32_t v) {                                                    // / 16 - 72
+  return h2_fma(nib_f16x2_hi(v), 0x2C002C00u, 0xD480D480u);
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where the 16 tokens of a tile lie: rows of the cache (all heads of all pages counted).
+// U16: page_size % 16 == 0, a tile never leaves its page.
+template <bool U16>
+struct Place {
+  uint32_t row0;       // U16: row of the tile's first token
+  bool ok;             // U16: its page exists
+};
+
+template <int KIND, int D, bool U16>
+struct Worker {
+  using C = Cfg<KIND, D>;
+  static constexpr bool kBf = KIND == W4_KV_BF16;
+  static constexpr int TT = C::TT, NG = C::NG, NV = C::NV, VW = C::VW, VE = C::VE, KW = C::KW;
+
+  const Args& a;
+  int lane, r, t;
+  int b, hk;
+  int lo, hi;                                     // visible tokens of this segment
+  uint32_t qf[D / 16][2];
+  float zmul[2];                                  // score -> log2 units, heads 2t and 2t + 1
+  float acc[D / 16][4];
+  float m[2], l[2];
+  int vexp;                                       // quantised: exponent of this output row's unit
+  uint32_t kw[TT][NG][2][KW];
+  uint32_t ksc[TT][2][kBf ? 1 : NG / 2];
+  uint32_t vw[TT][NV][4][VW];
+  uint32_t vsc[TT][NV][2];                        // bf16 pairs: tokens (2t, 2t+1), (2t+8, 2t+9)
+
+  __device__ __forceinline__ explicit Worker(const Args& args) : a(args) {
+    lane = threadIdx.x & 31;
+    r = lane >> 2;
+    t = lane & 3;
+  }
+
+  __device__ __forceinline__ void load_q(int head0, int heads) {
+    const uint16_t* row = a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(head0 + r) * D;
+    uint32_t w[NG][4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < heads) v = __ldg(reinterpret_cast<const uint4*>(row + 32 * g + 8 * t));
+      w[g][0] = v.x; w[g][1] = v.y; w[g][2] = v.z; w[g][3] = v.w;
+    }
+    const float base = a.scale * 1.4426950408889634f;
+    if constexpr (kBf) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) { qf[2 * g + s][0] = w[g][2 * s]; qf[2 * g + s][1] = w[g][2 * s + 1]; }
+      }
+      zmul[0] = zmul[1] = base;
+    } else {
+      // to fp16 with a power of two per head that brings the largest element to [2^14, 2^15)
+      uint32_t mx = 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = w[g][j] & 0x7FFFu, y = (w[g][j] >> 16) & 0x7FFFu;
+          if (x < 0x7F80u) mx = max(mx, x);
+          if (y < 0x7F80u) mx = max(mx, y);
+        }
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int f = shift_for(mx, 14);
+      const float up = pow2f(f);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if constexpr (KIND == W4_KV_INT8) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              qf[2 * g + s][i] = pack_h2(bf16_lo_to_f32(w[g][2 * s + i]) * up, bf16_hi_to_f32(w[g][2 * s + i]) * up);
+        } else {
+          uint32_t o[4];                           // pairs (0, 4), (1, 5), (2, 6), (3, 7): the nibbles' order
+          f16_pairs_l1(w[g], up, up, o);
+          qf[2 * g][0] = o[0]; qf[2 * g][1] = o[1]; qf[2 * g + 1][0] = o[2]; qf[2 * g + 1][1] = o[3];
+        }
+      }
+      const float down = base * pow2f(-f);
+      zmul[0] = __shfl_sync(0xffffffffu, down, 8 * t);
+      zmul[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+    }
+  }
+
+  __device__ __forceinline__ int page_at(int tok) const {
+    return __ldg(a.table + static_cast<int64_t>(b) * a.table_width + tok / a.page_size);
+  }
+  __device__ __forceinline__ bool page_ok(int page) const {
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages)) return true;
+    set_status(a.dev_status, W4_ERR_INVALID_ARG);
+    return false;
+  }
+  // U16: place of the tile that starts at tok (a multiple of 16)
+  __device__ __forceinline__ Place<U16> place(int tok) const {
+    Place<U16> p{0, false};
+    if (!U16 || tok >= hi || tok + 16 <= lo) return p;
+    const int page = page_at(tok);
+    p.ok = page_ok(page);
+    p.row0 = (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + tok % a.page_size;
+    return p;
+  }
+  // row of token tok0 + i; false where it is not to be looked at
+  __device__ __forceinline__ bool row_of(const Place<U16>& p, int tok0, int i, uint32_t& row) const {
+    const int tok = tok0 + i;
+    if (tok < lo || tok >= hi) return false;
+    if constexpr (U16) {
+      row = p.row0 + i;
+      return p.ok;
+    } else {
+      const int page = page_at(tok);
+      row = (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + tok % a.page_size;
+      return page_ok(page);
+    }
+  }
+
+  __device__ __forceinline__ void load_k(const Place<U16> (&p)[TT], int tok0) {
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t row = 0;
+        const bool ok = row_of(p[x], tok0 + 16 * x, r + 8 * h, row);
+        const uint32_t* at = static_cast<const uint32_t*>(a.k) + static_cast<uint64_t>(row) * C::ROWW + t * KW;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (ok) ldg_words<KW>(kw[x][g][h], at + 4 * g * KW);
+          else
+#pragma unroll
+            for (int i = 0; i < KW; ++i) kw[x][g][h][i] = 0;
+        }
+        if constexpr (!kBf) {
+          if (ok) ldg_scales<NG>(ksc[x][h], a.ks + static_cast<uint64_t>(row) * NG);
+          else
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) ksc[x][h][i] = 0;
+        }
+      }
+  }
+
+  __device__ __forceinline__ void load_v(const Place<U16> (&p)[TT], int tok0) {
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+      uint32_t sc[NV][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t row = 0;
+        const bool ok = row_of(p[x], tok0 + 16 * x, 2 * t + (i & 1) + 8 * (i >> 1), row);
+        const uint32_t* at = static_cast<const uint32_t*>(a.v) + static_cast<uint64_t>(row) * C::ROWW + r * VW;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (ok) ldg_words<VW>(vw[x][j][i], at + 8 * j * VW);
+          else
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[x][j][i][w] = 0;
+          if constexpr (!kBf)
+            sc[j][i] = ok ? __ldg(a.vs + static_cast<uint64_t>(row) * NG + (j * 8 + r) * VE / 32) : 0;
+        }
+      }
+      if constexpr (!kBf)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          vsc[x][j][0] = sc[j][0] | (sc[j][1] << 16);
+          vsc[x][j][1] = sc[j][2] | (sc[j][3] << 16);
+        }
+    }
+  }
+
+  __device__ __forceinline__ void scores(float (&s)[TT][4]) const {
+#pragma unroll
+    for (int x = 0; x < TT; ++x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const auto& k0 = kw[x][g][0];
+        const auto& k1 = kw[x][g][1];
+        if constexpr (kBf) {
+          mma_acc<true>(s[x], k0[0], k1[0], k0[1], k1[1], qf[2 * g][0], qf[2 * g][1]);
+          mma_acc<true>(s[x], k0[2], k1[2], k0[3], k1[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
+        } else {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (KIND == W4_KV_INT8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x0 = k0[h] ^ 0x80808080u, x1 = k1[h] ^ 0x80808080u;
+              mma_acc<false>(c, bytes_h2<0x4140>(x0), bytes_h2<0x4140>(x1), bytes_h2<0x4342>(x0), bytes_h2<0x4342>(x1),
+                             qf[2 * g + h][0], qf[2 * g + h][1]);
+            }
+          } else {
+            mma_acc<false>(c, nib_lo_h2(k0[0]), nib_lo_h2(k1[0]), nib_hi_h2(k0[0]), nib_hi_h2(k1[0]), qf[2 * g][0],
+                           qf[2 * g][1]);
+            const uint32_t x0 = k0[0] >> 8, x1 = k1[0] >> 8;
+            mma_acc<false>(c, nib_lo_h2(x0), nib_lo_h2(x1), nib_hi_h2(x0), nib_hi_h2(x1), qf[2 * g + 1][0],
+                           qf[2 * g + 1][1]);
+          }
+          const uint32_t w0 = ksc[x][0][g / 2], w1 = ksc[x][1][g / 2];
+          const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
+          const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
+          s[x][0] = fmaf(c[0], s0, s[x][0]);
+          s[x][1] = fmaf(c[1], s0, s[x][1]);
+          s[x][2] = fmaf(c[2], s1, s[x][2]);
+          s[x][3] = fmaf(c[3], s1, s[x][3]);
+        }
+      }
+    }
+  }
+
+  // scores -> weights: masks, the running reference, p in place of s
+  __device__ __forceinline__ void weights(const Place<U16> (&p)[TT], int tok0, float (&s)[TT][4]) {
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t row;
+        const bool ok = row_of(p[x], tok0 + 16 * x, r + 8 * h, row);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float z = s[x][2 * h + c] * zmul[c];
+          if (a.softcap > 0.f) {
+            const float cap = a.softcap * 1.4426950408889634f;
+            z = cap * tanhf(z / cap);
+          }
+          z = ok ? z : -INFINITY;
+          s[x][2 * h + c] = z;
+          mx[c] = fmaxf(mx[c], z);
+        }
+      }
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+        const float mn = fmaxf(m[c], mx[c]);
+        const float f = exp2_fast(m[c] - mn);
+        m[c] = mn;
+        l[c] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) { acc[i][c] *= f; acc[i][2 + c] *= f; }
+      }
+    }
+    const float ref[2] = {kBf ? m[0] : m[0] - kLift, kBf ? m[1] : m[1] - kLift};
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[x][i] = exp2_fast(s[x][i] - ref[i & 1]);
+        l[i & 1] += s[x][i];
+      }
+  }
+
+  __device__ __forceinline__ void outputs(const float (&s)[TT][4]) {
+    if constexpr (kBf) {
+#pragma unroll
+      for (int x = 0; x < TT; ++x) {
+        uint32_t hi_[2], lo_[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = pack_b2(s[x][2 * h], s[x][2 * h + 1]);
+          lo_[h] = transpose8(pack_b2(s[x][2 * h] - bf16_lo_to_f32(w), s[x][2 * h + 1] - bf16_hi_to_f32(w)));
+          hi_[h] = transpose8(w);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            const auto& v = vw[x][j];
+            const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410), a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+            const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410), a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+            mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, hi_[0], hi_[1]);
+            mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, lo_[0], lo_[1]);
+          }
+      }
+    } else {
+      // the unit of this output row: the largest finite scale seen so far in it
+      uint32_t e = 0;
+#pragma unroll
+      for (int x = 0; x < TT; ++x)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u = (vsc[x][j][h] >> 7) & 0xFFu, w = (vsc[x][j][h] >> 23) & 0xFFu;
+            if (u < 255u) e = max(e, u);
+            if (w < 255u) e = max(e, w);
+          }
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+      if (__any_sync(0xffffffffu, static_cast<int>(e) > vexp)) {
+        const int en = max(static_cast<int>(e), vexp);
+        const float f = exp2_fast(static_cast<float>(vexp - en));
+        vexp = en;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][c] *= f;
+      }
+      const float unit = pow2f(7 + 127 - vexp);          // largest scale to [2^7, 2^8)
+#pragma unroll
+      for (int x = 0; x < TT; ++x) {
+        const uint32_t p0 = transpose8(pack_h2(s[x][0], s[x][1])), p1 = transpose8(pack_h2(s[x][2], s[x][3]));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          uint32_t sv[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            sv[h] = pack_h2(bf16_lo_to_f32(vsc[x][j][h]) * unit, bf16_hi_to_f32(vsc[x][j][h]) * unit);
+          const auto& v = vw[x][j];
+          if constexpr (KIND == W4_KV_INT8) {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+              uint32_t el[2][4];                         // [token pair][element of the word]
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t x0 = v[2 * h][i] ^ 0x80808080u, x1 = v[2 * h + 1][i] ^ 0x80808080u;
+                const uint32_t u = __byte_perm(x0, x1, 0x5140), w = __byte_perm(x0, x1, 0x7362);
+                el[h][0] = h2_mul(bytes_h2<0x4140>(u), sv[h]);
+                el[h][1] = h2_mul(bytes_h2<0x4342>(u), sv[h]);
+                el[h][2] = h2_mul(bytes_h2<0x4140>(w), sv[h]);
+                el[h][3] = h2_mul(bytes_h2<0x4342>(w), sv[h]);
+              }
+              mma_acc<false>(acc[j * VE / 2 + 2 * i], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
+              mma_acc<false>(acc[j * VE / 2 + 2 * i + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {     // elements 0..3, 4..7 of the word
+                uint32_t el[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t u = __byte_perm(v[2 * h][i], v[2 * h + 1][i], half ? 0x7632 : 0x5410);
+                  el[h][0] = h2_mul(nib_lo_h2(u), sv[h]);
+                  el[h][1] = h2_mul(nib_hi_h2(u), sv[h]);
+                  el[h][2] = h2_mul(nib_lo_h2(u >> 8), sv[h]);
+                  el[h][3] = h2_mul(nib_hi_h2(u >> 8), sv[h]);
+                }
+                mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
+                mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
+              }
+          }
+        }
+      }
+    }
+  }
+
+  // every kWarps-th run of TT tiles from token t0 (a multiple of 16) on
+  __device__ __forceinline__ void walk(int t0, int warp) {
+    m[0] = m[1] = kLowest;
+    l[0] = l[1] = 0.f;
+    vexp = 8;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+    constexpr int kStep = 16 * TT;
+    int tok = t0 + warp * kStep;
+    if (tok >= hi) return;
+    Place<U16> p[TT];
+#pragma unroll
+    for (int x = 0; x < TT; ++x) p[x] = place(tok + 16 * x);
+    load_k(p, tok);
+    load_v(p, tok);
+    while (true) {
+      const int next = tok + kWarps * kStep;
+      Place<U16> pn[TT];
+#pragma unroll
+      for (int x = 0; x < TT; ++x) pn[x] = place(next + 16 * x);
+      float s[TT][4];
+      scores(s);
+      if (next < hi) load_k(pn, next);
+      weights(p, tok, s);
+      outputs(s);
+      if (next >= hi) break;
+      load_v(pn, next);
+#pragma unroll
+      for (int x = 0; x < TT; ++x) p[x] = pn[x];
+      tok = next;
+    }
+  }
+};
+
+template <int KIND, int D, bool U16>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel(const Args a) {
+  using C = Cfg<KIND, D>;
+  constexpr int kPitch = D + 4;
+  __shared__ float s_o[kWarps][kHeads][kPitch];
+  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+  __shared__ int s_scan[kWarps + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // this block's share of the line of units
+  const int per_seq = a.kv_heads * a.HB;
+  int64_t mine = 0;
+  for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) mine += span_of(a, b, blockIdx.x == 0).n;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  __shared__ int64_t s_sum[kWarps];
+  if (lane == 0) s_sum[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+  total *= per_seq;
+  const int64_t grid = total < gridDim.x ? total : gridDim.x;   // blocks with a share, at least a unit each
+  if (blockIdx.x >= grid) return;
+  int64_t at = total * blockIdx.x / grid;
+  const int64_t end = total * (blockIdx.x + 1) / grid;
+  // the sequence that holds unit `at`, and where its units begin
+  int b = 0;
+  int64_t begin = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32 * kWarps) {
+    const int mb = b0 + threadIdx.x;
+    int n = mb < a.B ? span_of(a, mb, false).n : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = inc;
+    if (threadIdx.x == 0) s_scan[0] = -1;
+    __syncthreads();
+    int64_t before = begin;
+    for (int w = 0; w < warp; ++w) before += s_sum[w] * per_seq;
+    const int64_t from = before + (inc - n) * per_seq;
+    if (n && at >= from && at < from + static_cast<int64_t>(n) * per_seq) {
+      s_scan[0] = mb;
+      s_scan[1] = static_cast<int>(at - from);           // below n * per_seq
+    }
+    __syncthreads();
+    if (s_scan[0] >= 0) break;
+    for (int w = 0; w < kWarps; ++w) begin += s_sum[w] * per_seq;
+  }
+  b = s_scan[0];
+  int64_t into = s_scan[1];
+  Span sp = span_of(a, b, false);
+  int item = static_cast<int>(into / sp.n);
+  int u = static_cast<int>(into - static_cast<int64_t>(item) * sp.n);
+
+  Worker<KIND, D, U16> w(a);
+  bool first_seg = true;
+  while (true) {
+    const int64_t left = end - at;
+    const int take = static_cast<int>(left < sp.n - u ? left : sp.n - u);
+    const int hk = item / a.HB, hb = item - hk * a.HB;
+    const int heads = min(kHeads, a.G - hb * kHeads);
+    const int head0 = hk * a.G + hb * kHeads;
+    w.b = b;
+    w.hk = hk;
+    const int t0 = (sp.u0 + u) * kUnit;
+    w.lo = max(sp.first, t0);
+    w.hi = min(sp.len, t0 + take * kUnit);
+    w.load_q(head0, heads);
+    w.walk(max(t0, w.lo & ~15), warp);
+
+    // join the warps: head h's reference is the largest of theirs
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) w.l[c] += __shfl_xor_sync(0xffffffffu, w.l[c], o);
+      if (w.r == 0) {
+        s_m[warp][2 * w.t + c] = w.m[c];
+        s_l[warp][2 * w.t + c] = w.l[c];
+      }
+    }
+    const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - 7);
+#pragma unroll
+    for (int j = 0; j < C::NV; ++j)
+#pragma unroll
+      for (int i = 0; i < C::VE / 2; ++i) {
+        const float* o = w.acc[j * C::VE / 2 + i];
+        const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
+        *reinterpret_cast<float2*>(&s_o[warp][2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
+        *reinterpret_cast<float2*>(&s_o[warp][2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
+      }
+    __syncthreads();
+    const bool whole = take == sp.n;
+    // a block continues an item in its slot 0 and begins one in its slot 1
+    float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (first_seg && u > 0 ? 0 : 1)) * kHeads * (D + 2);
+    for (int x = threadIdx.x; x < heads * (D / 4); x += 32 * kWarps) {
+      const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
+      float mm = kLowest, ll = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s_m[k][h]);
+      for (int k = 0; k < kWarps; ++k) {
+        const float f = exp2_fast(s_m[k][h] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[k][h][d]);
+        ll = fmaf(f, s_l[k][h], ll);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      if (whole) {
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const int64_t row = static_cast<int64_t>(b) * a.q_heads + head0 + h;
+        *reinterpret_cast<uint2*>(a.out + row * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (a.lse && d == 0)
+          a.lse[row] = ll > 0.f ? (mm - (KIND == W4_KV_BF16 ? 0.f : kLift) + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(part + h * D + d) = o;
+        if (d == 0) { part[kHeads * D + h] = mm; part[kHeads * D + kHeads + h] = ll; }
+      }
+    }
+    at += take;
+    first_seg = false;
+    if (at >= end) return;
+    u = 0;
+    if (++item == per_seq) {
+      item = 0;
+      do { sp = span_of(a, ++b, false); } while (sp.n == 0);
+    }
+    __syncthreads();
+  }
+}
+
+// One block per (sequence, query head): joins the parts of a split item in order, and writes the
+// zeros of an empty sequence.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, float lift) {
+  __shared__ int64_t s_sum[8];
+  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
+  const int hk = hq / a.G, hg = hq - hk * a.G, hb = hg / kHeads, h = hg - hb * kHeads;
+  int64_t before = 0, all = 0;
+  for (int i = threadIdx.x; i < a.B; i += 128) {
+    const int n = span_of(a, i, false).n;
+    all += n;
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) { s_sum[warp] = before; s_sum[4 + warp] = all; }
+  __syncthreads();
+  before = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  all = s_sum[4] + s_sum[5] + s_sum[6] + s_sum[7];
+  const int per_seq = a.kv_heads * a.HB;
+  const int64_t total = all * per_seq;
+  const int n = span_of(a, b, false).n;
+  const int64_t row = static_cast<int64_t>(b) * a.q_heads + hq;
+  if (n == 0) {
+    pdl_wait();                               // (every block: the call ends after both kernels)
+    for (int d = threadIdx.x; d < D / 2; d += 128) reinterpret_cast<uint32_t*>(a.out + row * D)[d] = 0u;
+    if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
+    return;
+  }
+  const int64_t start = before * per_seq + static_cast<int64_t>(hk * a.HB + hb) * n;
+  // block c of those with a share holds units [total c / grid, total (c + 1) / grid)
+  const int64_t grid = total < blocks ? total : blocks;
+  const int c0 = static_cast<int>(((start + 1) * grid - 1) / total);
+  const int c1 = static_cast<int>(((start + n) * grid - 1) / total);
+  pdl_wait();
+  if (c0 == c1) return;                       // written whole
+  constexpr int V = D / 32;
+  float o[V], m = kLowest, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const float* part = a.parts + static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * kHeads * (D + 2);
+    const float pm = part[kHeads * D + h], pl = part[kHeads * D + kHeads + h];
+    const float mn = fmaxf(m, pm), f = exp2_fast(m - mn), g = exp2_fast(pm - mn);
+    m = mn;
+    l = l * f + pl * g;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, part[h * D + lane + 32 * i] * g);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
+  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+  __syncthreads();
+  const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float ll = 0.f, f[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) { f[w] = exp2_fast(s_m[w] - mm); ll = fmaf(f[w], s_l[w], ll); }
+  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  for (int d = threadIdx.x; d < D; d += 128) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) x = fmaf(f[w], s_o[w][d], x);
+    a.out[row * D + d] = f32_to_bf16_bits(x * inv);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[row] = ll > 0.f ? (mm - lift + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+}
+
+// grid of the attention kernel: every SM filled, or one block a unit where there are fewer
+template <int KIND, int D>
+int grid_of(const Args& a, int sms) {
+  const int64_t units = static_cast<int64_t>(a.B) * a.kv_heads * a.HB *
+                        ((static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit);
+  const int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D>::MINB;
+  return static_cast<int>(units < most ? units : most);
+}
+
+template <int KIND, int D>
+w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
+  const int grid = grid_of<KIND, D>(a, sms);
+  if (a.page_size % 16 == 0) attend_kernel<KIND, D, true><<<grid, 32 * kWarps, 0, s>>>(a);
+  else attend_kernel<KIND, D, false><<<grid, 32 * kWarps, 0, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
+  const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
+  const unsigned rows = static_cast<unsigned>(a.B) * a.q_heads;
+  return launch_pdl(join_kernel<D>, dim3(rows), dim3(128), 0, s, a, grid, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int KIND>
+w4_status launch_kind(const Args& a, int D, cudaStream_t s, int sms) {
+  switch (D) {
+    case 64: return launch_dim<KIND, 64>(a, s, sms);
+    case 128: return launch_dim<KIND, 128>(a, s, sms);
+    case 192: return launch_dim<KIND, 192>(a, s, sms);
+    default: return launch_dim<KIND, 256>(a, s, sms);
+  }
+}
+
+w4_status launch_bf16(const Args& a, int D, cudaStream_t s, int sms);
+w4_status launch_int8(const Args& a, int D, cudaStream_t s, int sms);
+w4_status launch_int4(const Args& a, int D, cudaStream_t s, int sms);
+
+}  // namespace at
+}  // namespace w4

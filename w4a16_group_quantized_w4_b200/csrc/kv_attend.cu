@@ -57,6 +57,9 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
   a.dev_status = dev_status;
   a.G = q_heads / kv_heads;
   a.HB = (a.G + at::kHeads - 1) / at::kHeads;
+  a.div_shift = 0;
+  while ((1LL << a.div_shift) < page_size) ++a.div_shift;
+  a.div_mul = static_cast<uint32_t>((((1ULL << a.div_shift) - page_size) << 32) / page_size + 1);
   auto s = static_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
   return w4_record_status(kind == W4_KV_BF16 ? at::launch_bf16(a, head_dim, s, sms)

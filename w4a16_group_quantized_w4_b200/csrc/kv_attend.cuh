@@ -56,13 +56,20 @@ struct Args {
   int32_t* dev_status;
   // derived
   int G, HB;                          // query heads per key/value head, blocks of 8 of them
+  uint32_t div_mul;                   // token / page_size = (umulhi(token, div_mul) + token) >> div_shift
+  int div_shift;
 };
 
-// A sequence's visible tokens [first, len) and the units that cover them.
+__device__ __forceinline__ int page_of(const Args& a, int tok) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(tok), a.div_mul) + static_cast<uint32_t>(tok)) >> a.div_shift);
+}
+
+// A sequence's visible tokens [first, len), the n units that cover them, and the length of one of its
+// items on the line: n and the cost of beginning it.
 struct Span {
-  int first, len, u0, n;
+  int first, len, u0, n, line;
 };
-__device__ __forceinline__ Span span_of(const Args& a, int b, bool report) {
+__device__ __forceinline__ Span span_of(const Args& a, int b, int cost, bool report) {
   Span s;
   int len = __ldg(a.lens + b);
   const int most = a.table_width * a.page_size;
@@ -74,6 +81,7 @@ __device__ __forceinline__ Span span_of(const Args& a, int b, bool report) {
   s.first = a.window > 0 && len > a.window ? len - a.window : 0;
   s.u0 = s.first / kUnit;
   s.n = len > 0 ? (len + kUnit - 1) / kUnit - s.u0 : 0;
+  s.line = s.n ? s.n + cost : 0;
   return s;
 }
 
@@ -92,6 +100,10 @@ struct Cfg {
                             : KIND == W4_KV_INT8 ? (D == 64 ? 4 : D == 128 ? 2 : 1)
                             : (D == 64 ? 4 : D == 128 ? 4 : D == 192 ? 2 : 2);
   static constexpr int MINB = D == 64 ? 4 : D == 128 ? 3 : 2;                       // blocks per SM
+  // what beginning an item costs a block (its query, its first loads, its join), in units of tokens:
+  // the time of about 40 KB of the cache
+  static constexpr int kUnitBytes = 2 * kUnit * (4 * ROWW + (KIND == W4_KV_BF16 ? 0 : 2 * NG));
+  static constexpr int COST = (40000 + kUnitBytes / 2) / kUnitBytes > 1 ? (40000 + kUnitBytes / 2) / kUnitBytes : 1;
 };
 
 template <int W>
@@ -184,11 +196,18 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Where the 16 tokens of a tile lie: rows of the cache (all heads of all pages counted).
-// U16: page_size % 16 == 0, a tile never leaves its page.
+// D = A B in fp16 operands (the zero accumulator needs no registers)
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  mma_f16_16816(d, a, b0, b1, {0.f, 0.f, 0.f, 0.f});
+}
+
+// Where a 16-token tile lies.  Tokens outside [lo, hi) are replaced by the nearest one inside (their
+// weight is 0, and the stand-in's values are finite wherever the result is), so loads need no
+// predicate.  U16: page_size % 16 == 0, a tile never leaves its page.
 template <bool U16>
 struct Place {
-  uint32_t row0;       // U16: row of the tile's first token
+  int tok0;            // first token; a tile with nothing to see moves to the last one that has
+  uint32_t row0;       // U16: the cache row of tok0 (all heads of all pages counted)
   bool ok;             // U16: its page exists
 };
 
@@ -197,11 +216,13 @@ struct Worker {
   using C = Cfg<KIND, D>;
   static constexpr bool kBf = KIND == W4_KV_BF16;
   static constexpr int TT = C::TT, NG = C::NG, NV = C::NV, VW = C::VW, VE = C::VE, KW = C::KW;
+  static constexpr int kTileStep = 16 * kWarps;   // a warp's tiles alternate with the other warps'
 
   const Args& a;
   int lane, r, t;
   int b, hk;
   int lo, hi;                                     // visible tokens of this segment
+  uint32_t seen;                                  // bit 2x + h: token r + 8h of tile x counts
   uint32_t qf[D / 16][2];
   float zmul[2];                                  // score -> log2 units, heads 2t and 2t + 1
   float acc[D / 16][4];
@@ -270,78 +291,76 @@ struct Worker {
     }
   }
 
-  __device__ __forceinline__ int page_at(int tok) const {
-    return __ldg(a.table + static_cast<int64_t>(b) * a.table_width + tok / a.page_size);
-  }
   __device__ __forceinline__ bool page_ok(int page) const {
     if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages)) return true;
     set_status(a.dev_status, W4_ERR_INVALID_ARG);
     return false;
   }
-  // U16: place of the tile that starts at tok (a multiple of 16)
+  // cache row of tok; false (and row 0) where its page is not one of the cache
+  __device__ __forceinline__ bool row_at(int tok, uint32_t& row) const {
+    const int pi = page_of(a, tok);
+    const int page = __ldg(a.table + static_cast<int64_t>(b) * a.table_width + pi);
+    const bool ok = page_ok(page);
+    row = ok ? (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + (tok - pi * a.page_size) : 0u;
+    return ok;
+  }
+  // place of the tile that starts at tok (a multiple of 16)
   __device__ __forceinline__ Place<U16> place(int tok) const {
-    Place<U16> p{0, false};
-    if (!U16 || tok >= hi || tok + 16 <= lo) return p;
-    const int page = page_at(tok);
-    p.ok = page_ok(page);
-    p.row0 = (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + tok % a.page_size;
+    Place<U16> p;
+    p.tok0 = tok >= hi || tok + 16 <= lo ? (hi - 1) & ~15 : tok;
+    p.row0 = 0;
+    p.ok = true;
+    if constexpr (U16) p.ok = row_at(p.tok0, p.row0);
     return p;
   }
-  // row of token tok0 + i; false where it is not to be looked at
-  __device__ __forceinline__ bool row_of(const Place<U16>& p, int tok0, int i, uint32_t& row) const {
-    const int tok = tok0 + i;
-    if (tok < lo || tok >= hi) return false;
+  __device__ __forceinline__ bool row_of(const Place<U16>& p, int i, uint32_t& row) const {
+    const int tok = min(max(p.tok0 + i, lo), hi - 1);
     if constexpr (U16) {
-      row = p.row0 + i;
+      row = p.row0 + (tok - p.tok0);
+      if (!p.ok) row = 0;
       return p.ok;
     } else {
-      const int page = page_at(tok);
-      row = (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + tok % a.page_size;
-      return page_ok(page);
+      return row_at(tok, row);
     }
   }
 
   __device__ __forceinline__ void load_k(const Place<U16> (&p)[TT], int tok0) {
+    seen = 0;
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t row = 0;
-        const bool ok = row_of(p[x], tok0 + 16 * x, r + 8 * h, row);
+        uint32_t row;
+        const int tok = tok0 + x * kTileStep + r + 8 * h;
+        if (row_of(p[x], r + 8 * h, row) && tok >= lo && tok < hi) seen |= 1u << (2 * x + h);
         const uint32_t* at = static_cast<const uint32_t*>(a.k) + static_cast<uint64_t>(row) * C::ROWW + t * KW;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if (ok) ldg_words<KW>(kw[x][g][h], at + 4 * g * KW);
-          else
-#pragma unroll
-            for (int i = 0; i < KW; ++i) kw[x][g][h][i] = 0;
-        }
-        if constexpr (!kBf) {
-          if (ok) ldg_scales<NG>(ksc[x][h], a.ks + static_cast<uint64_t>(row) * NG);
-          else
-#pragma unroll
-            for (int i = 0; i < NG / 2; ++i) ksc[x][h][i] = 0;
-        }
+        for (int g = 0; g < NG; ++g) ldg_words<KW>(kw[x][g][h], at + 4 * g * KW);
+        if constexpr (!kBf) ldg_scales<NG>(ksc[x][h], a.ks + static_cast<uint64_t>(row) * NG);
       }
   }
 
-  __device__ __forceinline__ void load_v(const Place<U16> (&p)[TT], int tok0) {
+  __device__ __forceinline__ void load_v(const Place<U16> (&p)[TT]) {
 #pragma unroll
     for (int x = 0; x < TT; ++x) {
       uint32_t sc[NV][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t row = 0;
-        const bool ok = row_of(p[x], tok0 + 16 * x, 2 * t + (i & 1) + 8 * (i >> 1), row);
+        uint32_t row;
+        const bool ok = row_of(p[x], 2 * t + (i & 1) + 8 * (i >> 1), row);
         const uint32_t* at = static_cast<const uint32_t*>(a.v) + static_cast<uint64_t>(row) * C::ROWW + r * VW;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          if (ok) ldg_words<VW>(vw[x][j][i], at + 8 * j * VW);
-          else
+          ldg_words<VW>(vw[x][j][i], at + 8 * j * VW);
+          if constexpr (!kBf) sc[j][i] = __ldg(a.vs + static_cast<uint64_t>(row) * NG + (j * 8 + r) * VE / 32);
+        }
+        if (!ok) {                                     // a missing page: whatever row 0 holds must not count
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
 #pragma unroll
             for (int w = 0; w < VW; ++w) vw[x][j][i][w] = 0;
-          if constexpr (!kBf)
-            sc[j][i] = ok ? __ldg(a.vs + static_cast<uint64_t>(row) * NG + (j * 8 + r) * VE / 32) : 0;
+            sc[j][i] = 0;
+          }
         }
       }
       if constexpr (!kBf)
@@ -366,17 +385,18 @@ struct Worker {
           mma_acc<true>(s[x], k0[0], k1[0], k0[1], k1[1], qf[2 * g][0], qf[2 * g][1]);
           mma_acc<true>(s[x], k0[2], k1[2], k0[3], k1[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
         } else {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4];
           if constexpr (KIND == W4_KV_INT8) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t x0 = k0[h] ^ 0x80808080u, x1 = k1[h] ^ 0x80808080u;
-              mma_acc<false>(c, bytes_h2<0x4140>(x0), bytes_h2<0x4140>(x1), bytes_h2<0x4342>(x0), bytes_h2<0x4342>(x1),
-                             qf[2 * g + h][0], qf[2 * g + h][1]);
+              const uint32_t f[4] = {bytes_h2<0x4140>(x0), bytes_h2<0x4140>(x1), bytes_h2<0x4342>(x0), bytes_h2<0x4342>(x1)};
+              if (h == 0) mma_zero(c, f, qf[2 * g][0], qf[2 * g][1]);
+              else mma_acc<false>(c, f[0], f[1], f[2], f[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
             }
           } else {
-            mma_acc<false>(c, nib_lo_h2(k0[0]), nib_lo_h2(k1[0]), nib_hi_h2(k0[0]), nib_hi_h2(k1[0]), qf[2 * g][0],
-                           qf[2 * g][1]);
+            const uint32_t f[4] = {nib_lo_h2(k0[0]), nib_lo_h2(k1[0]), nib_hi_h2(k0[0]), nib_hi_h2(k1[0])};
+            mma_zero(c, f, qf[2 * g][0], qf[2 * g][1]);
             const uint32_t x0 = k0[0] >> 8, x1 = k1[0] >> 8;
             mma_acc<false>(c, nib_lo_h2(x0), nib_lo_h2(x1), nib_hi_h2(x0), nib_hi_h2(x1), qf[2 * g + 1][0],
                            qf[2 * g + 1][1]);
@@ -394,14 +414,13 @@ struct Worker {
   }
 
   // scores -> weights: masks, the running reference, p in place of s
-  __device__ __forceinline__ void weights(const Place<U16> (&p)[TT], int tok0, float (&s)[TT][4]) {
+  __device__ __forceinline__ void weights(uint32_t mask, float (&s)[TT][4]) {
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t row;
-        const bool ok = row_of(p[x], tok0 + 16 * x, r + 8 * h, row);
+        const bool ok = mask >> (2 * x + h) & 1u;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float z = s[x][2 * h + c] * zmul[c];
@@ -461,19 +480,25 @@ struct Worker {
       }
     } else {
       // the unit of this output row: the largest finite scale seen so far in it
-      uint32_t e = 0;
+      uint32_t pair = 0;
 #pragma unroll
       for (int x = 0; x < TT; ++x)
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) pair = __vmaxu2(pair, __vmaxu2(vsc[x][j][0], vsc[x][j][1]));
+      uint32_t e = max(pair & 0xFFFFu, pair >> 16);
+      if (e >= 0x7F80u) {                                // a scale of NaN or infinity: the largest finite one
+        e = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u = (vsc[x][j][h] >> 7) & 0xFFu, w = (vsc[x][j][h] >> 23) & 0xFFu;
-            if (u < 255u) e = max(e, u);
-            if (w < 255u) e = max(e, w);
+        for (int x = 0; x < TT; ++x)
+#pragma unroll
+          for (int j = 0; j < 2 * NV; ++j) {
+            const uint32_t w = vsc[x][j / 2][j & 1];
+            if ((w & 0xFFFFu) < 0x7F80u) e = max(e, w & 0xFFFFu);
+            if ((w >> 16) < 0x7F80u) e = max(e, w >> 16);
           }
+      }
       e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, 2)) >> 7;
       if (__any_sync(0xffffffffu, static_cast<int>(e) > vexp)) {
         const int en = max(static_cast<int>(e), vexp);
         const float f = exp2_fast(static_cast<float>(vexp - en));
@@ -533,7 +558,7 @@ struct Worker {
     }
   }
 
-  // every kWarps-th run of TT tiles from token t0 (a multiple of 16) on
+  // tiles warp, warp + kWarps, ... from token t0 (a multiple of 16) on, TT of them at once
   __device__ __forceinline__ void walk(int t0, int warp) {
     m[0] = m[1] = kLowest;
     l[0] = l[1] = 0.f;
@@ -542,28 +567,28 @@ struct Worker {
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
-    constexpr int kStep = 16 * TT;
-    int tok = t0 + warp * kStep;
+    int tok = t0 + warp * 16;
     if (tok >= hi) return;
     Place<U16> p[TT];
 #pragma unroll
-    for (int x = 0; x < TT; ++x) p[x] = place(tok + 16 * x);
+    for (int x = 0; x < TT; ++x) p[x] = place(tok + x * kTileStep);
     load_k(p, tok);
-    load_v(p, tok);
+    load_v(p);
     while (true) {
-      const int next = tok + kWarps * kStep;
-      Place<U16> pn[TT];
-#pragma unroll
-      for (int x = 0; x < TT; ++x) pn[x] = place(next + 16 * x);
+      const int next = tok + TT * kTileStep;
+      const bool more = next < hi;
       float s[TT][4];
       scores(s);
-      if (next < hi) load_k(pn, next);
-      weights(p, tok, s);
-      outputs(s);
-      if (next >= hi) break;
-      load_v(pn, next);
+      const uint32_t mask = seen;
+      if (more) {
 #pragma unroll
-      for (int x = 0; x < TT; ++x) p[x] = pn[x];
+        for (int x = 0; x < TT; ++x) p[x] = place(next + x * kTileStep);
+        load_k(p, next);
+      }
+      weights(mask, s);
+      outputs(s);
+      if (!more) break;
+      load_v(p);
       tok = next;
     }
   }
@@ -581,7 +606,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   // this block's share of the line of units
   const int per_seq = a.kv_heads * a.HB;
   int64_t mine = 0;
-  for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) mine += span_of(a, b, blockIdx.x == 0).n;
+  for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) mine += span_of(a, b, C::COST, blockIdx.x == 0).line;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   __shared__ int64_t s_sum[kWarps];
@@ -599,7 +624,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   int64_t begin = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32 * kWarps) {
     const int mb = b0 + threadIdx.x;
-    int n = mb < a.B ? span_of(a, mb, false).n : 0;
+    int n = mb < a.B ? span_of(a, mb, C::COST, false).line : 0;
     int64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -623,15 +648,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   }
   b = s_scan[0];
   int64_t into = s_scan[1];
-  Span sp = span_of(a, b, false);
-  int item = static_cast<int>(into / sp.n);
-  int u = static_cast<int>(into - static_cast<int64_t>(item) * sp.n);
+  Span sp = span_of(a, b, C::COST, false);
+  int item = static_cast<int>(into / sp.line);
+  int at_line = static_cast<int>(into - static_cast<int64_t>(item) * sp.line);   // place within the item
 
   Worker<KIND, D, U16> w(a);
-  bool first_seg = true;
   while (true) {
-    const int64_t left = end - at;
-    const int take = static_cast<int>(left < sp.n - u ? left : sp.n - u);
+    const int step = static_cast<int>(end - at < sp.line - at_line ? end - at : sp.line - at_line);
+    const int u = max(at_line - C::COST, 0), take = max(at_line + step - C::COST, 0) - u;   // units of it
     const int hk = item / a.HB, hb = item - hk * a.HB;
     const int heads = min(kHeads, a.G - hb * kHeads);
     const int head0 = hk * a.G + hb * kHeads;
@@ -640,66 +664,67 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
     const int t0 = (sp.u0 + u) * kUnit;
     w.lo = max(sp.first, t0);
     w.hi = min(sp.len, t0 + take * kUnit);
-    w.load_q(head0, heads);
-    w.walk(max(t0, w.lo & ~15), warp);
+    if (take > 0) {
+      w.load_q(head0, heads);
+      w.walk(max(t0, w.lo & ~15), warp);
 
-    // join the warps: head h's reference is the largest of theirs
+      // join the warps: head h's reference is the largest of theirs
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) w.l[c] += __shfl_xor_sync(0xffffffffu, w.l[c], o);
-      if (w.r == 0) {
-        s_m[warp][2 * w.t + c] = w.m[c];
-        s_l[warp][2 * w.t + c] = w.l[c];
+        for (int o = 4; o < 32; o <<= 1) w.l[c] += __shfl_xor_sync(0xffffffffu, w.l[c], o);
+        if (w.r == 0) {
+          s_m[warp][2 * w.t + c] = w.m[c];
+          s_l[warp][2 * w.t + c] = w.l[c];
+        }
+      }
+      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - 7);
+#pragma unroll
+      for (int j = 0; j < C::NV; ++j)
+#pragma unroll
+        for (int i = 0; i < C::VE / 2; ++i) {
+          const float* o = w.acc[j * C::VE / 2 + i];
+          const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
+          *reinterpret_cast<float2*>(&s_o[warp][2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
+          *reinterpret_cast<float2*>(&s_o[warp][2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
+        }
+      __syncthreads();
+      const bool whole = take == sp.n;
+      // a block continues an item in its slot 0 and begins one in its slot 1
+      float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (u > 0 ? 0 : 1)) * kHeads * (D + 2);
+      for (int x = threadIdx.x; x < heads * (D / 4); x += 32 * kWarps) {
+        const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
+        float mm = kLowest, ll = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s_m[k][h]);
+        for (int k = 0; k < kWarps; ++k) {
+          const float f = exp2_fast(s_m[k][h] - mm);
+          const float4 v = *reinterpret_cast<const float4*>(&s_o[k][h][d]);
+          ll = fmaf(f, s_l[k][h], ll);
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+        if (whole) {
+          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const int64_t row = static_cast<int64_t>(b) * a.q_heads + head0 + h;
+          *reinterpret_cast<uint2*>(a.out + row * D + d) =
+              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          if (a.lse && d == 0)
+            a.lse[row] = ll > 0.f ? (mm - (KIND == W4_KV_BF16 ? 0.f : kLift) + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(part + h * D + d) = o;
+          if (d == 0) { part[kHeads * D + h] = mm; part[kHeads * D + kHeads + h] = ll; }
+        }
       }
     }
-    const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - 7);
-#pragma unroll
-    for (int j = 0; j < C::NV; ++j)
-#pragma unroll
-      for (int i = 0; i < C::VE / 2; ++i) {
-        const float* o = w.acc[j * C::VE / 2 + i];
-        const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
-        *reinterpret_cast<float2*>(&s_o[warp][2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
-        *reinterpret_cast<float2*>(&s_o[warp][2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
-      }
-    __syncthreads();
-    const bool whole = take == sp.n;
-    // a block continues an item in its slot 0 and begins one in its slot 1
-    float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (first_seg && u > 0 ? 0 : 1)) * kHeads * (D + 2);
-    for (int x = threadIdx.x; x < heads * (D / 4); x += 32 * kWarps) {
-      const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
-      float mm = kLowest, ll = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s_m[k][h]);
-      for (int k = 0; k < kWarps; ++k) {
-        const float f = exp2_fast(s_m[k][h] - mm);
-        const float4 v = *reinterpret_cast<const float4*>(&s_o[k][h][d]);
-        ll = fmaf(f, s_l[k][h], ll);
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z);
-        o.w = fmaf(f, v.w, o.w);
-      }
-      if (whole) {
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
-        const int64_t row = static_cast<int64_t>(b) * a.q_heads + head0 + h;
-        *reinterpret_cast<uint2*>(a.out + row * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (a.lse && d == 0)
-          a.lse[row] = ll > 0.f ? (mm - (KIND == W4_KV_BF16 ? 0.f : kLift) + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-      } else {
-        *reinterpret_cast<float4*>(part + h * D + d) = o;
-        if (d == 0) { part[kHeads * D + h] = mm; part[kHeads * D + kHeads + h] = ll; }
-      }
-    }
-    at += take;
-    first_seg = false;
+    at += step;
     if (at >= end) return;
-    u = 0;
+    at_line = 0;
     if (++item == per_seq) {
       item = 0;
-      do { sp = span_of(a, ++b, false); } while (sp.n == 0);
+      do { sp = span_of(a, ++b, C::COST, false); } while (sp.n == 0);
     }
     __syncthreads();
   }
@@ -708,7 +733,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
 // One block per (sequence, query head): joins the parts of a split item in order, and writes the
 // zeros of an empty sequence.
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, float lift) {
+__global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, int cost, float lift) {
   __shared__ int64_t s_sum[8];
   __shared__ float s_o[4][D], s_m[4], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -716,7 +741,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, flo
   const int hk = hq / a.G, hg = hq - hk * a.G, hb = hg / kHeads, h = hg - hb * kHeads;
   int64_t before = 0, all = 0;
   for (int i = threadIdx.x; i < a.B; i += 128) {
-    const int n = span_of(a, i, false).n;
+    const int n = span_of(a, i, cost, false).line;
     all += n;
     if (i < b) before += n;
   }
@@ -731,7 +756,8 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, flo
   all = s_sum[4] + s_sum[5] + s_sum[6] + s_sum[7];
   const int per_seq = a.kv_heads * a.HB;
   const int64_t total = all * per_seq;
-  const int n = span_of(a, b, false).n;
+  const Span sp = span_of(a, b, cost, false);
+  const int n = sp.n;
   const int64_t row = static_cast<int64_t>(b) * a.q_heads + hq;
   if (n == 0) {
     pdl_wait();                               // (every block: the call ends after both kernels)
@@ -739,8 +765,8 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, flo
     if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
     return;
   }
-  const int64_t start = before * per_seq + static_cast<int64_t>(hk * a.HB + hb) * n;
-  // block c of those with a share holds units [total c / grid, total (c + 1) / grid)
+  const int64_t start = before * per_seq + static_cast<int64_t>(hk * a.HB + hb) * sp.line + cost;   // its first unit
+  // block c of those with a share holds [total c / grid, total (c + 1) / grid) of the line
   const int64_t grid = total < blocks ? total : blocks;
   const int c0 = static_cast<int>(((start + 1) * grid - 1) / total);
   const int c1 = static_cast<int>(((start + n) * grid - 1) / total);
@@ -794,7 +820,7 @@ w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
   const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
   const unsigned rows = static_cast<unsigned>(a.B) * a.q_heads;
-  return launch_pdl(join_kernel<D>, dim3(rows), dim3(128), 0, s, a, grid, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+  return launch_pdl(join_kernel<D>, dim3(rows), dim3(128), 0, s, a, grid, Cfg<KIND, D>::COST, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 template <int KIND>

@@ -3,18 +3,20 @@
 //   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(z_t - m),  z_t = log2(e) * cap(scale * q . k_t)
 //
 // One pass over the cache with a running reference m per head.  Bound by the cache's bytes, each of
-// which is needed once, so nothing is staged in shared memory: the tensor-core operands are loaded
-// straight from global memory into the registers of the lanes that feed them.
+// which is needed once.  Every warp streams its own tokens, 16 at a time, through its own ring of
+// stages in shared memory (cp.async, whole rows, so that many bytes are in flight without registers
+// and without a block-wide wait) and reads tensor-core operands from there as whole words:
 //   * Scores, S^T = K Q^T: tokens are the 16 rows of an m16n8k16 product, up to 8 query heads of one
 //     key/value head its 8 columns.  The product does not care in which order the head dimension
 //     is summed, so lane (r, t) = (lane / 4, lane % 4) takes the 8 consecutive elements 32 g + 8 t of
-//     token rows r and r + 8: a quad reads 64 (bf16), 32 (int8) or 16 (int4) contiguous bytes a row.
+//     token rows r and r + 8.
 //   * Outputs, O^T = V^T P^T: head-dimension elements are the 16 rows, tokens the 16 summed ones.  Lane
-//     (r, t) loads VE consecutive elements at VE r of tokens 2t, 2t+1, 2t+8, 2t+9 (eight lanes read
-//     whole 128-byte lines where a row has them) and byte permutes pair the tokens up.
+//     (r, t) takes VE consecutive elements at VE r of tokens 2t, 2t+1, 2t+8, 2t+9; byte permutes pair
+//     the tokens up.
+// Rows lie in shared memory at a pitch that keeps both reads free of bank conflicts.
 //   * The weights p leave the first product with tokens along r and enter the second with tokens
 //     along t: one 8x8 register transpose (movmatrix) per 8 tokens.
-// Codes are widened to fp16 exactly.  Key scales multiply the float32 sum of their group; value
+// Codes are widened to fp16 exactly (a bias is taken back later).  Key scales multiply the float32 sum of their group; value
 // scales multiply the widened code in fp16, brought into range by a power of two per output row
 // (one more rounding of 2^-11; scaling the weights instead would need a weight per group).  Weights are
 // rounded to fp16 against quantised values; against bf16 values they enter as a bf16 pair (high and
@@ -38,6 +40,7 @@ constexpr int kHeads = 8;             // query heads an item
 constexpr int64_t kMostTokens = 0x7FFFEFFF;   // a sequence's table: token numbers stay below 2^31 past its end
 constexpr float kLowest = -3.0e38f;   // reference before any token: finite, so that masked scores give p = 0
 constexpr float kSlack = 8.f;         // a reference is raised once a score passes it by 2^kSlack
+constexpr int kScaleTop = 4;           // value scales in fp16: 1536 * 2^5 is below its largest number
 constexpr float kLift = 6.f;          // weights for fp16 are taken times 2^kLift: at most 2^14
 
 struct Args {
@@ -85,6 +88,11 @@ __device__ __forceinline__ Span span_of(const Args& a, int b, int cost, bool rep
   return s;
 }
 
+// [kind][head_dim / 64 - 1]
+constexpr int kTiles[3][4] = {{1, 1, 1, 1}, {2, 1, 1, 1}, {2, 2, 1, 1}};
+constexpr int kStages[3][4] = {{3, 5, 4, 3}, {3, 3, 3, 3}, {4, 3, 3, 4}};
+constexpr int kBlocks[3][4] = {{3, 1, 1, 1}, {3, 3, 2, 2}, {4, 3, 3, 2}};
+
 template <int KIND, int D>
 struct Cfg {
   static constexpr int KW = KIND == W4_KV_BF16 ? 4 : KIND == W4_KV_INT8 ? 2 : 1;   // words per 8 elements
@@ -95,11 +103,18 @@ struct Cfg {
                             : (D % 256 == 0 ? 32 : D % 128 == 0 ? 16 : 8);
   static constexpr int VW = VE / 8 * KW;
   static constexpr int NV = D / (8 * VE);
-  // 16-token tiles a warp takes at once: about 4 KB of keys and as much of values in flight
-  static constexpr int TT = KIND == W4_KV_BF16 ? (D == 64 ? 2 : 1)
-                            : KIND == W4_KV_INT8 ? (D == 64 ? 4 : D == 128 ? 2 : 1)
-                            : (D == 64 ? 4 : D == 128 ? 4 : D == 192 ? 2 : 2);
-  static constexpr int MINB = D == 64 ? 4 : D == 128 ? 3 : 2;                       // blocks per SM
+  static constexpr int CPR = ROWW / 4;                                              // 16-byte chunks per row
+  static constexpr int LC = CPR & -CPR;                                             // lanes that copy a row together
+  // pitches in chunks: a key read of 8 rows and a value read of 4 cover all banks once
+  static constexpr int PK = KIND == W4_KV_BF16 ? CPR + 4 : KIND == W4_KV_INT8 ? CPR + 2 : CPR + 1;
+  static constexpr int PV = CPR + 1;
+  static constexpr int kTileBytes = 16 * 16 * (PK + PV) + (KIND == W4_KV_BF16 ? 0 : 16 * 4 * NG);
+  static constexpr int TT = kTiles[KIND][D / 64 - 1];       // tiles a stage
+  static constexpr int S = kStages[KIND][D / 64 - 1];       // stages of a warp's ring
+  static constexpr int MINB = kBlocks[KIND][D / 64 - 1];    // blocks per SM
+  static constexpr int kStage = TT * kTileBytes;
+  static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
+  static constexpr int kSmem = kWarps * S * kStage > kJoin ? kWarps * S * kStage : kJoin;
   // what beginning an item costs a block (its query, its first loads, its join), in units of tokens:
   // the time of about 40 KB of the cache
   static constexpr int kUnitBytes = 2 * kUnit * (4 * ROWW + (KIND == W4_KV_BF16 ? 0 : 2 * NG));
@@ -107,39 +122,39 @@ struct Cfg {
 };
 
 template <int W>
-__device__ __forceinline__ void ldg_words(uint32_t (&o)[W], const uint32_t* p) {
+__device__ __forceinline__ void lds_words(uint32_t (&o)[W], uint32_t at) {
   if constexpr (W == 4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = lds128(at);
     o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
   } else if constexpr (W == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = lds64(at);
     o[0] = v.x; o[1] = v.y;
   } else {
-    o[0] = __ldg(p);
+    o[0] = lds32(at);
   }
 }
-
-// NG bf16 scales of a row as (NG + 1) / 2 words
+// NG bf16 scales of a row as words
 template <int NG>
-__device__ __forceinline__ void ldg_scales(uint32_t (&o)[NG / 2], const uint16_t* p) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-  if constexpr (NG == 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w));
-    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-  } else if constexpr (NG == 4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(w));
-    o[0] = v.x; o[1] = v.y;
-  } else {
+__device__ __forceinline__ void lds_scales(uint32_t (&o)[NG / 2], uint32_t at) {
+  if constexpr (NG == 8 || NG == 4) lds_words<NG / 2>(o, at);
+  else
 #pragma unroll
-    for (int i = 0; i < NG / 2; ++i) o[i] = __ldg(w + i);
-  }
+    for (int i = 0; i < NG / 2; ++i) o[i] = lds32(at + 4 * i);
 }
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -150,15 +165,35 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// bytes (already offset by 128) 0, 1 or 2, 3 of v -> fp16 pair of the signed values, exactly:
-// 0x6400 | u is 1024 + u
+// Codes as exact fp16 numbers with a bias.  The bits of a code go into the low (or upper) mantissa of a
+// power of two; the bias leaves again in float32 (keys: with the product's C operand) or in the fused
+// multiply by the scale (values), where it must be exact in fp16 after that multiplication.
+//
+// Keys, int8: bytes offset by 128, 0x6400 | u = 1024 + u = 1152 + code.
+constexpr float kKeyBias8 = 1152.f;
 template <int SEL>
-__device__ __forceinline__ uint32_t bytes_h2(uint32_t v) {
-  return h2_add(__byte_perm(v, 0x64646464u, SEL), 0xE480E480u);        // - 1152
+__device__ __forceinline__ uint32_t key_bytes(uint32_t v) { return __byte_perm(v, 0x64646464u, SEL); }
+// Keys, int4: nibbles at bits 4..7 of each half, 0x5400 | u << 4 = 64 + u = 72 + code.
+constexpr float kKeyBias4 = 72.f;
+__device__ __forceinline__ uint32_t key_nibbles(uint32_t v) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x00F000F0u), "r"(0x54005400u));
+  return r;
 }
-__device__ __forceinline__ uint32_t nib_lo_h2(uint32_t v) { return h2_add(nib_f16x2_lo(v), 0xE408E408u); }   // - 1032
-__device__ __forceinline__ uint32_t nib_hi_h2(uint32_t v) {                                                    // / 16 - 72
-  return h2_fma(nib_f16x2_hi(v), 0x2C002C00u, 0xD480D480u);
+// Values, int8: bytes sign-extended to 16 bits, (b & 0x3FF) ^ 0x6600 = 1536 + code; 1536 = 3 * 512, so
+// 1536 * scale has 10 significant bits at most and fma(x, s, -1536 s) is code * s rounded once.
+template <int SEL>
+__device__ __forceinline__ uint32_t value_bytes(uint32_t a, uint32_t b, uint32_t s, uint32_t bias) {
+  uint32_t e, r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(e) : "r"(a), "r"(b), "n"(SEL));   // (selector bit 3: the byte's sign)
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(e), "r"(0x03FF03FFu), "r"(0x66006600u));
+  return h2_fma(r, s, bias);
+}
+// Values, int4: nibbles at bits 6..9, 0x4C00 | u << 6 = 16 + u = 24 + code, likewise with 24 = 3 * 8.
+__device__ __forceinline__ uint32_t value_nibbles(uint32_t v, uint32_t s, uint32_t bias) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x03C003C0u), "r"(0x4C004C00u));
+  return h2_fma(r, s, bias);
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t d;
@@ -196,21 +231,6 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// D = A B in fp16 operands (the zero accumulator needs no registers)
-__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  mma_f16_16816(d, a, b0, b1, {0.f, 0.f, 0.f, 0.f});
-}
-
-// Where a 16-token tile lies.  Tokens outside [lo, hi) are replaced by the nearest one inside (their
-// weight is 0, and the stand-in's values are finite wherever the result is), so loads need no
-// predicate.  U16: page_size % 16 == 0, a tile never leaves its page.
-template <bool U16>
-struct Place {
-  int tok0;            // first token; a tile with nothing to see moves to the last one that has
-  uint32_t row0;       // U16: the cache row of tok0 (all heads of all pages counted)
-  bool ok;             // U16: its page exists
-};
-
 template <int KIND, int D, bool U16>
 struct Worker {
   using C = Cfg<KIND, D>;
@@ -222,16 +242,14 @@ struct Worker {
   int lane, r, t;
   int b, hk;
   int lo, hi;                                     // visible tokens of this segment
-  uint32_t seen;                                  // bit 2x + h: token r + 8h of tile x counts
+  uint32_t ring;                                  // this warp's stages in shared memory
+  uint32_t* marks;                                // per stage: bit 16 x + i, token i of tile x counts
   uint32_t qf[D / 16][2];
+  float qb[kBf ? 1 : NG][2];                      // quantised: minus the keys' bias times a group's sum of q
   float zmul[2];                                  // score -> log2 units, heads 2t and 2t + 1
   float acc[D / 16][4];
   float m[2], l[2];
   int vexp;                                       // quantised: exponent of this output row's unit
-  uint32_t kw[TT][NG][2][KW];
-  uint32_t ksc[TT][2][kBf ? 1 : NG / 2];
-  uint32_t vw[TT][NV][4][VW];
-  uint32_t vsc[TT][NV][2];                        // bf16 pairs: tokens (2t, 2t+1), (2t+8, 2t+9)
 
   __device__ __forceinline__ explicit Worker(const Args& args) : a(args) {
     lane = threadIdx.x & 31;
@@ -285,123 +303,162 @@ struct Worker {
           qf[2 * g][0] = o[0]; qf[2 * g][1] = o[1]; qf[2 * g + 1][0] = o[2]; qf[2 * g + 1][1] = o[3];
         }
       }
+      // sums of the fp16 queries over each group, for heads 2t and 2t + 1
+      constexpr float kBias = KIND == W4_KV_INT8 ? kKeyBias8 : kKeyBias4;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&qf[2 * g + i / 2][i & 1]));
+          sum += v.x + v.y;
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qb[g][0] = -kBias * __shfl_sync(0xffffffffu, sum, 8 * t);
+        qb[g][1] = -kBias * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      }
       const float down = base * pow2f(-f);
       zmul[0] = __shfl_sync(0xffffffffu, down, 8 * t);
       zmul[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }
   }
 
+  __device__ __forceinline__ int page_entry(int tok) const {
+    return __ldg(a.table + static_cast<int64_t>(b) * a.table_width + page_of(a, tok));
+  }
   __device__ __forceinline__ bool page_ok(int page) const {
     if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages)) return true;
     set_status(a.dev_status, W4_ERR_INVALID_ARG);
     return false;
   }
-  // cache row of tok; false (and row 0) where its page is not one of the cache
-  __device__ __forceinline__ bool row_at(int tok, uint32_t& row) const {
-    const int pi = page_of(a, tok);
-    const int page = __ldg(a.table + static_cast<int64_t>(b) * a.table_width + pi);
-    const bool ok = page_ok(page);
-    row = ok ? (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + (tok - pi * a.page_size) : 0u;
-    return ok;
+  // cache row (all heads of all pages counted) of tok on its page
+  __device__ __forceinline__ uint32_t row_on(int page, int tok) const {
+    return (static_cast<uint32_t>(page) * a.kv_heads + hk) * a.page_size + (tok - page_of(a, tok) * a.page_size);
   }
-  // place of the tile that starts at tok (a multiple of 16)
-  __device__ __forceinline__ Place<U16> place(int tok) const {
-    Place<U16> p;
-    p.tok0 = tok >= hi || tok + 16 <= lo ? (hi - 1) & ~15 : tok;
-    p.row0 = 0;
-    p.ok = true;
-    if constexpr (U16) p.ok = row_at(p.tok0, p.row0);
-    return p;
-  }
-  __device__ __forceinline__ bool row_of(const Place<U16>& p, int i, uint32_t& row) const {
-    const int tok = min(max(p.tok0 + i, lo), hi - 1);
+  // The page entries of the TT tiles from tok on, loaded a step before they are needed.  Page sizes
+  // that are no multiple of 16 need one per token: lane l takes token l % 16 of tile l / 16.
+  struct Pages {
+    int e[U16 ? TT : 1];
+  };
+  __device__ __forceinline__ int lane_tok(int tok) const { return tok + (lane >> 4) * kTileStep + (lane & 15); }
+  __device__ __forceinline__ int inside(int tok) const { return min(max(tok, lo), hi - 1); }
+  __device__ __forceinline__ void look_up(Pages& p, int tok) const {
     if constexpr (U16) {
-      row = p.row0 + (tok - p.tok0);
-      if (!p.ok) row = 0;
-      return p.ok;
+#pragma unroll
+      for (int x = 0; x < TT; ++x) p.e[x] = page_entry(inside(tok + x * kTileStep));
     } else {
-      return row_at(tok, row);
+      p.e[0] = page_entry(inside(lane_tok(tok)));
     }
   }
 
-  __device__ __forceinline__ void load_k(const Place<U16> (&p)[TT], int tok0) {
-    seen = 0;
+  // copies the TT tiles from tok on into stage st
+  __device__ __forceinline__ void fetch(const Pages& p, int tok, int st) {
+    const uint32_t base = ring + st * C::kStage;
+    const auto* kc = static_cast<const uint8_t*>(a.k);
+    const auto* vc = static_cast<const uint8_t*>(a.v);
+    constexpr int kRowB = 4 * C::ROWW, LC = C::LC, RPI = 32 / LC;
+    const int lrow = lane / LC, lcol = lane % LC;
+    bool whole = U16 && tok >= lo && tok + (TT - 1) * kTileStep + 16 <= hi;
+    if constexpr (U16) {
 #pragma unroll
-    for (int x = 0; x < TT; ++x)
+      for (int x = 0; x < TT; ++x) whole = whole && static_cast<unsigned>(p.e[x]) < static_cast<unsigned>(a.pages);
+    }
+    if (whole) {                                    // 16 rows that follow one another
+      if (lane == 0) marks[st] = ~0u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t row;
-        const int tok = tok0 + x * kTileStep + r + 8 * h;
-        if (row_of(p[x], r + 8 * h, row) && tok >= lo && tok < hi) seen |= 1u << (2 * x + h);
-        const uint32_t* at = static_cast<const uint32_t*>(a.k) + static_cast<uint64_t>(row) * C::ROWW + t * KW;
+      for (int x = 0; x < TT; ++x) {
+        const uint32_t row0 = row_on(p.e[U16 ? x : 0], tok + x * kTileStep);
+        const uint32_t ks = base + x * C::kTileBytes, vs = ks + 256 * C::PK, ss = vs + 256 * C::PV;
+        const uint64_t off = static_cast<uint64_t>(row0 + lrow) * kRowB + lcol * 16;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) ldg_words<KW>(kw[x][g][h], at + 4 * g * KW);
-        if constexpr (!kBf) ldg_scales<NG>(ksc[x][h], a.ks + static_cast<uint64_t>(row) * NG);
-      }
-  }
-
-  __device__ __forceinline__ void load_v(const Place<U16> (&p)[TT]) {
+        for (int y = 0; y < 16 / RPI; ++y)
 #pragma unroll
-    for (int x = 0; x < TT; ++x) {
-      uint32_t sc[NV][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t row;
-        const bool ok = row_of(p[x], 2 * t + (i & 1) + 8 * (i >> 1), row);
-        const uint32_t* at = static_cast<const uint32_t*>(a.v) + static_cast<uint64_t>(row) * C::ROWW + r * VW;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          ldg_words<VW>(vw[x][j][i], at + 8 * j * VW);
-          if constexpr (!kBf) sc[j][i] = __ldg(a.vs + static_cast<uint64_t>(row) * NG + (j * 8 + r) * VE / 32);
-        }
-        if (!ok) {                                     // a missing page: whatever row 0 holds must not count
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-#pragma unroll
-            for (int w = 0; w < VW; ++w) vw[x][j][i][w] = 0;
-            sc[j][i] = 0;
+          for (int c = 0; c < C::CPR / LC; ++c) {
+            copy_async<16>(ks + ((y * RPI + lrow) * C::PK + c * LC + lcol) * 16, kc + off + y * RPI * kRowB + c * LC * 16);
+            copy_async<16>(vs + ((y * RPI + lrow) * C::PV + c * LC + lcol) * 16, vc + off + y * RPI * kRowB + c * LC * 16);
+          }
+        if constexpr (!kBf) {
+          if (lane < 4 * NG) {
+            const uint16_t* sc = lane < 2 * NG ? a.ks : a.vs;
+            const int c = lane < 2 * NG ? lane : lane - 2 * NG;
+            copy_async<16>(ss + lane * 16, sc + static_cast<uint64_t>(row0) * NG + c * 8);
           }
         }
       }
-      if constexpr (!kBf)
+      return;
+    }
+    // token by token: lane l knows the row of token l % 16 of tile l / 16 (row 0, to be left out, for none)
+    static_assert(TT <= 2, "a warp's lanes and a mark's bits hold two tiles");
+    const int want = lane_tok(tok), at = inside(want);
+    int page;
+    if constexpr (U16) page = page_entry(at);
+    else page = p.e[0];
+    bool ok = want >= lo && want < hi;
+    if (ok) ok = page_ok(page);
+    const uint32_t row = ok ? row_on(page, at) : 0u;
+    const uint32_t mark = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) marks[st] = mark;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          vsc[x][j][0] = sc[j][0] | (sc[j][1] << 16);
-          vsc[x][j][1] = sc[j][2] | (sc[j][3] << 16);
+    for (int x = 0; x < TT; ++x) {
+      const uint32_t ks = base + x * C::kTileBytes, vs = ks + 256 * C::PK, ss = vs + 256 * C::PV;
+#pragma unroll
+      for (int y = 0; y < 16 / RPI; ++y) {
+        const uint32_t rr = __shfl_sync(0xffffffffu, row, x * 16 + y * RPI + lrow);
+        const uint64_t off = static_cast<uint64_t>(rr) * kRowB + lcol * 16;
+#pragma unroll
+        for (int c = 0; c < C::CPR / LC; ++c) {
+          copy_async<16>(ks + ((y * RPI + lrow) * C::PK + c * LC + lcol) * 16, kc + off + c * LC * 16);
+          copy_async<16>(vs + ((y * RPI + lrow) * C::PV + c * LC + lcol) * 16, vc + off + c * LC * 16);
         }
+      }
+      if constexpr (!kBf) {
+#pragma unroll
+        for (int y = 0; y < NG / 2; ++y) {                // 4-byte words: 8 NG of the keys', then the values'
+          const int w = 32 * y + lane, v = w >= 8 * NG, i = w - v * 8 * NG, tk = i / (NG / 2), col = i - tk * (NG / 2);
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, x * 16 + tk);
+          copy_async<4>(ss + w * 4, (v ? a.vs : a.ks) + static_cast<uint64_t>(rr) * NG + 2 * col);
+        }
+      }
     }
   }
 
-  __device__ __forceinline__ void scores(float (&s)[TT][4]) const {
+  __device__ __forceinline__ void scores(uint32_t base, float (&s)[TT][4]) const {
 #pragma unroll
     for (int x = 0; x < TT; ++x) {
+      const uint32_t ks = base + x * C::kTileBytes + r * (C::PK * 16) + t * (4 * KW);
+      const uint32_t ss = base + x * C::kTileBytes + 256 * (C::PK + C::PV) + r * (2 * NG);
+      uint32_t ksc[2][kBf ? 1 : NG / 2];
+      if constexpr (!kBf) {
+        lds_scales<NG>(ksc[0], ss);
+        lds_scales<NG>(ksc[1], ss + 16 * NG);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const auto& k0 = kw[x][g][0];
-        const auto& k1 = kw[x][g][1];
+        uint32_t k0[KW], k1[KW];
+        lds_words<KW>(k0, ks + 16 * g * KW);
+        lds_words<KW>(k1, ks + 8 * 16 * C::PK + 16 * g * KW);
         if constexpr (kBf) {
           mma_acc<true>(s[x], k0[0], k1[0], k0[1], k1[1], qf[2 * g][0], qf[2 * g][1]);
           mma_acc<true>(s[x], k0[2], k1[2], k0[3], k1[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
         } else {
-          float c[4];
+          float c[4] = {qb[g][0], qb[g][1], qb[g][0], qb[g][1]};
           if constexpr (KIND == W4_KV_INT8) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t x0 = k0[h] ^ 0x80808080u, x1 = k1[h] ^ 0x80808080u;
-              const uint32_t f[4] = {bytes_h2<0x4140>(x0), bytes_h2<0x4140>(x1), bytes_h2<0x4342>(x0), bytes_h2<0x4342>(x1)};
-              if (h == 0) mma_zero(c, f, qf[2 * g][0], qf[2 * g][1]);
-              else mma_acc<false>(c, f[0], f[1], f[2], f[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
+              mma_acc<false>(c, key_bytes<0x4140>(x0), key_bytes<0x4140>(x1), key_bytes<0x4342>(x0), key_bytes<0x4342>(x1),
+                             qf[2 * g + h][0], qf[2 * g + h][1]);
             }
           } else {
-            const uint32_t f[4] = {nib_lo_h2(k0[0]), nib_lo_h2(k1[0]), nib_hi_h2(k0[0]), nib_hi_h2(k1[0])};
-            mma_zero(c, f, qf[2 * g][0], qf[2 * g][1]);
-            const uint32_t x0 = k0[0] >> 8, x1 = k1[0] >> 8;
-            mma_acc<false>(c, nib_lo_h2(x0), nib_lo_h2(x1), nib_hi_h2(x0), nib_hi_h2(x1), qf[2 * g + 1][0],
-                           qf[2 * g + 1][1]);
+            mma_acc<false>(c, key_nibbles(k0[0] << 4), key_nibbles(k1[0] << 4), key_nibbles(k0[0]), key_nibbles(k1[0]),
+                           qf[2 * g][0], qf[2 * g][1]);
+            mma_acc<false>(c, key_nibbles(k0[0] >> 4), key_nibbles(k1[0] >> 4), key_nibbles(k0[0] >> 8),
+                           key_nibbles(k1[0] >> 8), qf[2 * g + 1][0], qf[2 * g + 1][1]);
           }
-          const uint32_t w0 = ksc[x][0][g / 2], w1 = ksc[x][1][g / 2];
+          const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
           const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
           const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
           s[x][0] = fmaf(c[0], s0, s[x][0]);
@@ -419,20 +476,25 @@ struct Worker {
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool ok = mask >> (2 * x + h) & 1u;
+      for (int i = 0; i < 4; ++i) s[x][i] *= zmul[i & 1];
+    if (a.softcap > 0.f) {
+      const float cap = a.softcap * 1.4426950408889634f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float z = s[x][2 * h + c] * zmul[c];
-          if (a.softcap > 0.f) {
-            const float cap = a.softcap * 1.4426950408889634f;
-            z = cap * tanhf(z / cap);
-          }
-          z = ok ? z : -INFINITY;
-          s[x][2 * h + c] = z;
-          mx[c] = fmaxf(mx[c], z);
-        }
-      }
+      for (int x = 0; x < TT; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] = cap * tanhf(s[x][i] / cap);
+    }
+    if (mask != ~0u) {
+#pragma unroll
+      for (int x = 0; x < TT; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(mask >> (16 * x + r + 8 * (i / 2)) & 1u)) s[x][i] = -INFINITY;
+    }
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[x][i]);
     if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -456,7 +518,22 @@ struct Worker {
       }
   }
 
-  __device__ __forceinline__ void outputs(const float (&s)[TT][4]) {
+  // The tokens 2t, 2t + 1, 2t + 8, 2t + 9 of tile x in the j-th chunk of columns; zeros where one does not count.
+  __device__ __forceinline__ void values(uint32_t base, uint32_t mask, int x, int j, uint32_t (&v)[4][VW]) const {
+    const uint32_t at = base + x * C::kTileBytes + 256 * C::PK + t * (2 * C::PV * 16) + (8 * j + r) * (4 * VW);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds_words<VW>(v[i], at + ((i & 1) + 8 * (i >> 1)) * (C::PV * 16));
+    if (mask != ~0u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(mask >> (16 * x + 2 * t + (i & 1) + 8 * (i >> 1)) & 1u)) {
+#pragma unroll
+          for (int w = 0; w < VW; ++w) v[i][w] = 0;
+        }
+    }
+  }
+
+  __device__ __forceinline__ void outputs(uint32_t base, uint32_t mask, const float (&s)[TT][4]) {
     if constexpr (kBf) {
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
@@ -468,17 +545,34 @@ struct Worker {
           hi_[h] = transpose8(w);
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+          uint32_t v[4][VW];
+          values(base, mask, x, j, v);
 #pragma unroll
           for (int i = 0; i < VW; ++i) {
-            const auto& v = vw[x][j];
             const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410), a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
             const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410), a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
             mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, hi_[0], hi_[1]);
             mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, lo_[0], lo_[1]);
           }
+        }
       }
     } else {
+      uint32_t vsc[TT][NV][2];                           // bf16 pairs: tokens (2t, 2t+1), (2t+8, 2t+9)
+#pragma unroll
+      for (int x = 0; x < TT; ++x)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t at = base + x * C::kTileBytes + 256 * (C::PK + C::PV) + 32 * NG + t * (4 * NG) + (j * 8 + r) * VE / 32 * 2;
+          uint32_t sc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[i] = lds_u16(at + ((i & 1) + 8 * (i >> 1)) * (2 * NG));
+            if (mask != ~0u && !(mask >> (16 * x + 2 * t + (i & 1) + 8 * (i >> 1)) & 1u)) sc[i] = 0;
+          }
+          vsc[x][j][0] = sc[0] | (sc[1] << 16);
+          vsc[x][j][1] = sc[2] | (sc[3] << 16);
+        }
       // the unit of this output row: the largest finite scale seen so far in it
       uint32_t pair = 0;
 #pragma unroll
@@ -508,50 +602,50 @@ struct Worker {
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[i][c] *= f;
       }
-      const float unit = pow2f(7 + 127 - vexp);          // largest scale to [2^7, 2^8)
+      const float unit = pow2f(kScaleTop + 127 - vexp);  // largest scale to [2^kScaleTop, 2 * 2^kScaleTop)
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
         const uint32_t p0 = transpose8(pack_h2(s[x][0], s[x][1])), p1 = transpose8(pack_h2(s[x][2], s[x][3]));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          uint32_t sv[2];
+          uint32_t sv[2], bias[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
             sv[h] = pack_h2(bf16_lo_to_f32(vsc[x][j][h]) * unit, bf16_hi_to_f32(vsc[x][j][h]) * unit);
-          const auto& v = vw[x][j];
-          if constexpr (KIND == W4_KV_INT8) {
+            bias[h] = h2_mul(sv[h], KIND == W4_KV_INT8 ? 0xE600E600u : 0xCE00CE00u);   // -1536, -24: exact
+          }
+          uint32_t v[4][VW];
+          values(base, mask, x, j, v);
 #pragma unroll
-            for (int i = 0; i < VW; ++i) {
+          for (int i = 0; i < VW; ++i) {
+            if constexpr (KIND == W4_KV_INT8) {
               uint32_t el[2][4];                         // [token pair][element of the word]
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t x0 = v[2 * h][i] ^ 0x80808080u, x1 = v[2 * h + 1][i] ^ 0x80808080u;
-                const uint32_t u = __byte_perm(x0, x1, 0x5140), w = __byte_perm(x0, x1, 0x7362);
-                el[h][0] = h2_mul(bytes_h2<0x4140>(u), sv[h]);
-                el[h][1] = h2_mul(bytes_h2<0x4342>(u), sv[h]);
-                el[h][2] = h2_mul(bytes_h2<0x4140>(w), sv[h]);
-                el[h][3] = h2_mul(bytes_h2<0x4342>(w), sv[h]);
+                const uint32_t wa = v[2 * h][i], wb = v[2 * h + 1][i];
+                el[h][0] = value_bytes<0xC480>(wa, wb, sv[h], bias[h]);
+                el[h][1] = value_bytes<0xD591>(wa, wb, sv[h], bias[h]);
+                el[h][2] = value_bytes<0xE6A2>(wa, wb, sv[h], bias[h]);
+                el[h][3] = value_bytes<0xF7B3>(wa, wb, sv[h], bias[h]);
               }
               mma_acc<false>(acc[j * VE / 2 + 2 * i], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
               mma_acc<false>(acc[j * VE / 2 + 2 * i + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < VW; ++i)
+            } else {
 #pragma unroll
               for (int half = 0; half < 2; ++half) {     // elements 0..3, 4..7 of the word
                 uint32_t el[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const uint32_t u = __byte_perm(v[2 * h][i], v[2 * h + 1][i], half ? 0x7632 : 0x5410);
-                  el[h][0] = h2_mul(nib_lo_h2(u), sv[h]);
-                  el[h][1] = h2_mul(nib_hi_h2(u), sv[h]);
-                  el[h][2] = h2_mul(nib_lo_h2(u >> 8), sv[h]);
-                  el[h][3] = h2_mul(nib_hi_h2(u >> 8), sv[h]);
+                  el[h][0] = value_nibbles(u << 6, sv[h], bias[h]);
+                  el[h][1] = value_nibbles(u << 2, sv[h], bias[h]);
+                  el[h][2] = value_nibbles(u >> 2, sv[h], bias[h]);
+                  el[h][3] = value_nibbles(u >> 6, sv[h], bias[h]);
                 }
                 mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
                 mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
               }
+            }
           }
         }
       }
@@ -562,43 +656,56 @@ struct Worker {
   __device__ __forceinline__ void walk(int t0, int warp) {
     m[0] = m[1] = kLowest;
     l[0] = l[1] = 0.f;
-    vexp = 8;
+    vexp = kScaleTop + 1;                            // (2^(kScaleTop + 127 - vexp) stays a float)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
     int tok = t0 + warp * 16;
     if (tok >= hi) return;
-    Place<U16> p[TT];
+    constexpr int kStep = TT * kTileStep;
+    Pages p;
+    int ahead = tok;                                   // where the next stage begins
 #pragma unroll
-    for (int x = 0; x < TT; ++x) p[x] = place(tok + x * kTileStep);
-    load_k(p, tok);
-    load_v(p);
-    while (true) {
-      const int next = tok + TT * kTileStep;
-      const bool more = next < hi;
-      float s[TT][4];
-      scores(s);
-      const uint32_t mask = seen;
-      if (more) {
-#pragma unroll
-        for (int x = 0; x < TT; ++x) p[x] = place(next + x * kTileStep);
-        load_k(p, next);
+    for (int st = 0; st < C::S - 1; ++st) {
+      if (ahead < hi) {
+        look_up(p, ahead);
+        fetch(p, ahead, st);
       }
-      weights(mask, s);
-      outputs(s);
-      if (!more) break;
-      load_v(p);
-      tok = next;
+      copy_commit();
+      ahead += kStep;
     }
+    look_up(p, ahead);
+    int st = 0, into = C::S - 1;                       // the stage at hand, and the one consumed last
+    while (true) {
+      copy_wait<C::S - 2>();
+      __syncwarp();
+      if (ahead < hi) {
+        fetch(p, ahead, into);
+        look_up(p, ahead + kStep);
+      }
+      copy_commit();
+      const uint32_t base = ring + st * C::kStage, mask = marks[st];
+      float s[TT][4];
+      scores(base, s);
+      weights(mask, s);
+      outputs(base, mask, s);
+      tok += kStep;
+      if (tok >= hi) break;
+      ahead += kStep;
+      into = st;
+      st = st + 1 == C::S ? 0 : st + 1;
+    }
+    copy_wait<0>();
   }
 };
 
 template <int KIND, int D, bool U16>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel(const Args a) {
   using C = Cfg<KIND, D>;
-  constexpr int kPitch = D + 4;
-  __shared__ float s_o[kWarps][kHeads][kPitch];
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  auto& s_o = *reinterpret_cast<float(*)[kWarps][kHeads][D + 4]>(s_ring);   // once the stages are done with
+  __shared__ uint32_t s_marks[kWarps][C::S];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   __shared__ int s_scan[kWarps + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -653,6 +760,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   int at_line = static_cast<int>(into - static_cast<int64_t>(item) * sp.line);   // place within the item
 
   Worker<KIND, D, U16> w(a);
+  w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
+  w.marks = s_marks[warp];
   while (true) {
     const int step = static_cast<int>(end - at < sp.line - at_line ? end - at : sp.line - at_line);
     const int u = max(at_line - C::COST, 0), take = max(at_line + step - C::COST, 0) - u;   // units of it
@@ -669,6 +778,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
       w.walk(max(t0, w.lo & ~15), warp);
 
       // join the warps: head h's reference is the largest of theirs
+      __syncthreads();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -678,7 +788,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
           s_l[warp][2 * w.t + c] = w.l[c];
         }
       }
-      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - 7);
+      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop);
 #pragma unroll
       for (int j = 0; j < C::NV; ++j)
 #pragma unroll
@@ -815,8 +925,11 @@ int grid_of(const Args& a, int sms) {
 template <int KIND, int D>
 w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
   const int grid = grid_of<KIND, D>(a, sms);
-  if (a.page_size % 16 == 0) attend_kernel<KIND, D, true><<<grid, 32 * kWarps, 0, s>>>(a);
-  else attend_kernel<KIND, D, false><<<grid, 32 * kWarps, 0, s>>>(a);
+  auto kernel = a.page_size % 16 == 0 ? attend_kernel<KIND, D, true> : attend_kernel<KIND, D, false>;
+  constexpr int kSmem = Cfg<KIND, D>::kSmem;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return W4_ERR_CUDA;
+  kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
   const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
   const unsigned rows = static_cast<unsigned>(a.B) * a.q_heads;

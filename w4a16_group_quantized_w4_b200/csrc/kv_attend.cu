@@ -53,7 +53,8 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
   a.window = window;
   a.out = out;
   a.lse = lse;
-  a.parts = static_cast<float*>(workspace);
+  a.recs = static_cast<at::Rec*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + at::recs_bytes(device_sm_count()));
   a.dev_status = dev_status;
   a.G = q_heads / kv_heads;
   a.HB = (a.G + at::kHeads - 1) / at::kHeads;
@@ -67,9 +68,10 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
                                                : at::launch_int4(a, head_dim, s, sms));
 }
 
-// Two parts (a block's first and last item) of kHeads heads for every block of the largest grid.
+// A record and two parts (of a block's first and last item) of kHeads heads for every block of the largest grid.
 size_t w4_attend_workspace_bytes(int64_t B, int64_t q_heads, int64_t head_dim, int64_t kv_heads) {
   if (B < 1 || q_heads < 1 || kv_heads < 1 || head_dim < 64 || head_dim > 256) return 0;
-  const int64_t blocks = static_cast<int64_t>(w4::device_sm_count()) * 4;
-  return static_cast<size_t>(2 * blocks * w4::at::kHeads * (head_dim + 2) * 4);
+  const int sms = w4::device_sm_count();
+  const int64_t blocks = static_cast<int64_t>(sms) * w4::at::kMostBlocks;
+  return static_cast<size_t>(w4::at::recs_bytes(sms) + 2 * blocks * w4::at::kHeads * (head_dim + 2) * 4);
 }

@@ -40,8 +40,11 @@ constexpr int kHeads = 8;             // query heads an item
 constexpr int64_t kMostTokens = 0x7FFFEFFF;   // a sequence's table: token numbers stay below 2^31 past its end
 constexpr float kLowest = -3.0e38f;   // reference before any token: finite, so that masked scores give p = 0
 constexpr float kSlack = 8.f;         // a reference is raised once a score passes it by 2^kSlack
-constexpr int kScaleTop = 4;           // value scales in fp16: 1536 * 2^5 is below its largest number
 constexpr float kLift = 6.f;          // weights for fp16 are taken times 2^kLift: at most 2^14
+
+struct Rec {
+  int b, item, last;                  // last: the last block that holds a part, -1 for nothing to join
+};
 
 struct Args {
   const uint16_t* q;
@@ -56,6 +59,7 @@ struct Args {
   uint16_t* out;
   float* lse;
   float* parts;                       // [2 * grid][kHeads * (D + 2)]: sums, references, totals
+  Rec* recs;                          // [grid]
   int32_t* dev_status;
   // derived
   int G, HB;                          // query heads per key/value head, blocks of 8 of them
@@ -88,10 +92,13 @@ __device__ __forceinline__ Span span_of(const Args& a, int b, int cost, bool rep
   return s;
 }
 
+constexpr int kMostBlocks = 4;        // of one SM, in kBlocks
+inline int64_t recs_bytes(int sms) { return (static_cast<int64_t>(sms) * kMostBlocks * sizeof(Rec) + 15) / 16 * 16; }
+
 // [kind][head_dim / 64 - 1]
 constexpr int kTiles[3][4] = {{1, 1, 1, 1}, {2, 1, 1, 1}, {2, 2, 1, 1}};
-constexpr int kStages[3][4] = {{3, 5, 4, 3}, {3, 3, 3, 3}, {4, 3, 3, 4}};
-constexpr int kBlocks[3][4] = {{3, 1, 1, 1}, {3, 3, 2, 2}, {4, 3, 3, 2}};
+constexpr int kStages[3][4] = {{3, 5, 4, 3}, {3, 3, 3, 3}, {3, 3, 3, 3}};
+constexpr int kBlocks[3][4] = {{3, 1, 1, 1}, {3, 3, 2, 2}, {4, 3, 4, 3}};
 
 template <int KIND, int D>
 struct Cfg {
@@ -112,6 +119,7 @@ struct Cfg {
   static constexpr int TT = kTiles[KIND][D / 64 - 1];       // tiles a stage
   static constexpr int S = kStages[KIND][D / 64 - 1];       // stages of a warp's ring
   static constexpr int MINB = kBlocks[KIND][D / 64 - 1];    // blocks per SM
+  static_assert(MINB <= kMostBlocks, "the workspace has room for kMostBlocks an SM");
   static constexpr int kStage = TT * kTileBytes;
   static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
   static constexpr int kSmem = kWarps * S * kStage > kJoin ? kWarps * S * kStage : kJoin;
@@ -165,21 +173,20 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// Codes as exact fp16 numbers with a bias.  The bits of a code go into the low (or upper) mantissa of a
-// power of two; the bias leaves again in float32 (keys: with the product's C operand) or in the fused
-// multiply by the scale (values), where it must be exact in fp16 after that multiplication.
+// Codes as exact fp16 numbers with a bias.  The bits of a code go into the mantissa of a power of two or
+// of a subnormal number; the bias leaves again in float32 (keys: with the product's C operand) or in the
+// fused multiply by the scale (values), where it must be exact in fp16 after that multiplication.
 //
 // Keys, int8: bytes offset by 128, 0x6400 | u = 1024 + u = 1152 + code.
-constexpr float kKeyBias8 = 1152.f;
 template <int SEL>
 __device__ __forceinline__ uint32_t key_bytes(uint32_t v) { return __byte_perm(v, 0x64646464u, SEL); }
-// Keys, int4: nibbles at bits 4..7 of each half, 0x5400 | u << 4 = 64 + u = 72 + code.
-constexpr float kKeyBias4 = 72.f;
-__device__ __forceinline__ uint32_t key_nibbles(uint32_t v) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x00F000F0u), "r"(0x54005400u));
-  return r;
-}
+// int4: a nibble at bits 0..3 of a half is the subnormal u 2^-24, at bits 4..7 u 2^-20, with u = code + 8:
+// one AND each, and a single shift by 8 for the other two nibbles of the half.
+__device__ __forceinline__ uint32_t nib0(uint32_t v) { return v & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t nib1(uint32_t v) { return v & 0x00F000F0u; }
+// what a key product's bias is, per unit of the queries' sum
+template <int KIND>
+constexpr float kKeyBias = KIND == W4_KV_INT8 ? 1152.f : 8.f / 16777216.f;
 // Values, int8: bytes sign-extended to 16 bits, (b & 0x3FF) ^ 0x6600 = 1536 + code; 1536 = 3 * 512, so
 // 1536 * scale has 10 significant bits at most and fma(x, s, -1536 s) is code * s rounded once.
 template <int SEL>
@@ -189,12 +196,10 @@ __device__ __forceinline__ uint32_t value_bytes(uint32_t a, uint32_t b, uint32_t
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(e), "r"(0x03FF03FFu), "r"(0x66006600u));
   return h2_fma(r, s, bias);
 }
-// Values, int4: nibbles at bits 6..9, 0x4C00 | u << 6 = 16 + u = 24 + code, likewise with 24 = 3 * 8.
-__device__ __forceinline__ uint32_t value_nibbles(uint32_t v, uint32_t s, uint32_t bias) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x03C003C0u), "r"(0x4C004C00u));
-  return h2_fma(r, s, bias);
-}
+// Value scales in fp16: the largest of an output row is brought to [2^kScaleTop, 2 * 2^kScaleTop).  int8:
+// 1536 times it is below fp16's largest number; int4: 2^24 times it is.
+template <int KIND>
+constexpr int kScaleTop = KIND == W4_KV_INT8 ? 4 : -10;
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -236,6 +241,7 @@ struct Worker {
   using C = Cfg<KIND, D>;
   static constexpr bool kBf = KIND == W4_KV_BF16;
   static constexpr int TT = C::TT, NG = C::NG, NV = C::NV, VW = C::VW, VE = C::VE, KW = C::KW;
+  static constexpr int kUnitTop = KIND == W4_KV_INT4 ? kScaleTop<KIND> + 24 : kScaleTop<KIND>;   // of the factor's scale
   static constexpr int kTileStep = 16 * kWarps;   // a warp's tiles alternate with the other warps'
 
   const Args& a;
@@ -298,27 +304,27 @@ struct Worker {
             for (int i = 0; i < 2; ++i)
               qf[2 * g + s][i] = pack_h2(bf16_lo_to_f32(w[g][2 * s + i]) * up, bf16_hi_to_f32(w[g][2 * s + i]) * up);
         } else {
-          uint32_t o[4];                           // pairs (0, 4), (1, 5), (2, 6), (3, 7): the nibbles' order
-          f16_pairs_l1(w[g], up, up, o);
+          // pairs (0, 4), (1, 5), (2, 6), (3, 7), the nibbles' order; those read at bits 4..7 divided by 16
+          uint32_t o[4];
+          f16_pairs_l1(w[g], up, up * 0.0625f, o);
           qf[2 * g][0] = o[0]; qf[2 * g][1] = o[1]; qf[2 * g + 1][0] = o[2]; qf[2 * g + 1][1] = o[3];
         }
       }
       // sums of the fp16 queries over each group, for heads 2t and 2t + 1
-      constexpr float kBias = KIND == W4_KV_INT8 ? kKeyBias8 : kKeyBias4;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&qf[2 * g + i / 2][i & 1]));
-          sum += v.x + v.y;
+          sum += (KIND == W4_KV_INT4 && (i & 1) ? 16.f : 1.f) * (v.x + v.y);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qb[g][0] = -kBias * __shfl_sync(0xffffffffu, sum, 8 * t);
-        qb[g][1] = -kBias * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        qb[g][0] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
+        qb[g][1] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       }
-      const float down = base * pow2f(-f);
+      const float down = base * pow2f(-f) * (KIND == W4_KV_INT4 ? 16777216.f : 1.f);
       zmul[0] = __shfl_sync(0xffffffffu, down, 8 * t);
       zmul[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }
@@ -453,10 +459,9 @@ struct Worker {
                              qf[2 * g + h][0], qf[2 * g + h][1]);
             }
           } else {
-            mma_acc<false>(c, key_nibbles(k0[0] << 4), key_nibbles(k1[0] << 4), key_nibbles(k0[0]), key_nibbles(k1[0]),
-                           qf[2 * g][0], qf[2 * g][1]);
-            mma_acc<false>(c, key_nibbles(k0[0] >> 4), key_nibbles(k1[0] >> 4), key_nibbles(k0[0] >> 8),
-                           key_nibbles(k1[0] >> 8), qf[2 * g + 1][0], qf[2 * g + 1][1]);
+            mma_acc<false>(c, nib0(k0[0]), nib0(k1[0]), nib1(k0[0]), nib1(k1[0]), qf[2 * g][0], qf[2 * g][1]);
+            mma_acc<false>(c, nib0(k0[0] >> 8), nib0(k1[0] >> 8), nib1(k0[0] >> 8), nib1(k1[0] >> 8), qf[2 * g + 1][0],
+                           qf[2 * g + 1][1]);
           }
           const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
           const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
@@ -602,7 +607,7 @@ struct Worker {
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[i][c] *= f;
       }
-      const float unit = pow2f(kScaleTop + 127 - vexp);  // largest scale to [2^kScaleTop, 2 * 2^kScaleTop)
+      const float unit = pow2f(kUnitTop + 127 - vexp);
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
         const uint32_t p0 = transpose8(pack_h2(s[x][0], s[x][1])), p1 = transpose8(pack_h2(s[x][2], s[x][3]));
@@ -612,7 +617,8 @@ struct Worker {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             sv[h] = pack_h2(bf16_lo_to_f32(vsc[x][j][h]) * unit, bf16_hi_to_f32(vsc[x][j][h]) * unit);
-            bias[h] = h2_mul(sv[h], KIND == W4_KV_INT8 ? 0xE600E600u : 0xCE00CE00u);   // -1536, -24: exact
+            // int8: -1536 s.  int4: sv is 2^24 s, the factor of bits 0..3; -8 s = -2^-21 sv
+            bias[h] = h2_mul(sv[h], KIND == W4_KV_INT8 ? 0xE600E600u : 0x80088008u);
           }
           uint32_t v[4][VW];
           values(base, mask, x, j, v);
@@ -637,10 +643,11 @@ struct Worker {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const uint32_t u = __byte_perm(v[2 * h][i], v[2 * h + 1][i], half ? 0x7632 : 0x5410);
-                  el[h][0] = value_nibbles(u << 6, sv[h], bias[h]);
-                  el[h][1] = value_nibbles(u << 2, sv[h], bias[h]);
-                  el[h][2] = value_nibbles(u >> 2, sv[h], bias[h]);
-                  el[h][3] = value_nibbles(u >> 6, sv[h], bias[h]);
+                  const uint32_t s1 = h2_mul(sv[h], 0x2C002C00u);       // 2^20 s, the factor of bits 4..7
+                  el[h][0] = h2_fma(nib0(u), sv[h], bias[h]);
+                  el[h][1] = h2_fma(nib1(u), s1, bias[h]);
+                  el[h][2] = h2_fma(nib0(u >> 8), sv[h], bias[h]);
+                  el[h][3] = h2_fma(nib1(u >> 8), s1, bias[h]);
                 }
                 mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
                 mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
@@ -653,10 +660,10 @@ struct Worker {
   }
 
   // tiles warp, warp + kWarps, ... from token t0 (a multiple of 16) on, TT of them at once
-  __device__ __forceinline__ void walk(int t0, int warp) {
+  __device__ __forceinline__ void walk(int t0, int warp, int head0, int heads) {
     m[0] = m[1] = kLowest;
     l[0] = l[1] = 0.f;
-    vexp = kScaleTop + 1;                            // (2^(kScaleTop + 127 - vexp) stays a float)
+    vexp = kUnitTop + 1;                             // (2^(kUnitTop + 127 - vexp) stays a float)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -664,18 +671,18 @@ struct Worker {
     int tok = t0 + warp * 16;
     if (tok >= hi) return;
     constexpr int kStep = TT * kTileStep;
-    Pages p;
+    Pages p, first[C::S - 1];
+#pragma unroll
+    for (int st = 0; st < C::S - 1; ++st) look_up(first[st], tok + st * kStep);
     int ahead = tok;                                   // where the next stage begins
 #pragma unroll
     for (int st = 0; st < C::S - 1; ++st) {
-      if (ahead < hi) {
-        look_up(p, ahead);
-        fetch(p, ahead, st);
-      }
+      if (ahead < hi) fetch(first[st], ahead, st);
       copy_commit();
       ahead += kStep;
     }
     look_up(p, ahead);
+    load_q(head0, heads);                              // while the first stages are on their way
     int st = 0, into = C::S - 1;                       // the stage at hand, and the one consumed last
     while (true) {
       copy_wait<C::S - 2>();
@@ -707,57 +714,73 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   auto& s_o = *reinterpret_cast<float(*)[kWarps][kHeads][D + 4]>(s_ring);   // once the stages are done with
   __shared__ uint32_t s_marks[kWarps][C::S];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-  __shared__ int s_scan[kWarps + 2];
+  __shared__ int s_scan[2];
+  __shared__ int64_t s_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // this block's share of the line of units
+  pdl_trigger();                                       // (the joining blocks wait for this grid's end)
+  // This block's share of the line.  Every thread adds up its run of sequences; the one whose run holds
+  // the share's first place looks it up in there.
   const int per_seq = a.kv_heads * a.HB;
+  const int run = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = threadIdx.x * run, b1 = min(b0 + run, a.B);
   int64_t mine = 0;
-  for (int b = threadIdx.x; b < a.B; b += 32 * kWarps) mine += span_of(a, b, C::COST, blockIdx.x == 0).line;
+  for (int i = b0; i < b1; ++i) mine += span_of(a, i, C::COST, blockIdx.x == 0).line;
+  int64_t upto = mine;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  __shared__ int64_t s_sum[kWarps];
-  if (lane == 0) s_sum[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) s_sum[warp] = upto;
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+  for (int k = 0; k < kWarps; ++k) {
+    if (k < warp) upto += s_sum[k];
+    total += s_sum[k];
+  }
   total *= per_seq;
+  // the rows of sequences without tokens
+  for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
+    if (__ldg(a.lens + i) > 0) continue;
+    uint32_t* row = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(i) * a.q_heads * D);
+    for (int x = threadIdx.x; x < a.q_heads * (D / 2); x += 32 * kWarps) row[x] = 0u;
+    if (a.lse)
+      for (int x = threadIdx.x; x < a.q_heads; x += 32 * kWarps) a.lse[static_cast<int64_t>(i) * a.q_heads + x] = -INFINITY;
+  }
   const int64_t grid = total < gridDim.x ? total : gridDim.x;   // blocks with a share, at least a unit each
-  if (blockIdx.x >= grid) return;
+  if (blockIdx.x >= grid) {
+    if (threadIdx.x == 0) a.recs[blockIdx.x].last = -1;
+    return;
+  }
   int64_t at = total * blockIdx.x / grid;
   const int64_t end = total * (blockIdx.x + 1) / grid;
-  // the sequence that holds unit `at`, and where its units begin
-  int b = 0;
-  int64_t begin = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32 * kWarps) {
-    const int mb = b0 + threadIdx.x;
-    int n = mb < a.B ? span_of(a, mb, C::COST, false).line : 0;
-    int64_t inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+  int64_t from = (upto - mine) * per_seq;
+  if (at >= from && at < upto * per_seq) {
+    int i = b0;
+    for (;; ++i) {
+      const int64_t n = static_cast<int64_t>(span_of(a, i, C::COST, false).line) * per_seq;
+      if (at < from + n) break;
+      from += n;
     }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = inc;
-    if (threadIdx.x == 0) s_scan[0] = -1;
-    __syncthreads();
-    int64_t before = begin;
-    for (int w = 0; w < warp; ++w) before += s_sum[w] * per_seq;
-    const int64_t from = before + (inc - n) * per_seq;
-    if (n && at >= from && at < from + static_cast<int64_t>(n) * per_seq) {
-      s_scan[0] = mb;
-      s_scan[1] = static_cast<int>(at - from);           // below n * per_seq
-    }
-    __syncthreads();
-    if (s_scan[0] >= 0) break;
-    for (int w = 0; w < kWarps; ++w) begin += s_sum[w] * per_seq;
+    s_scan[0] = i;
+    s_scan[1] = static_cast<int>(at - from);             // below 2^31: the tokens' limit
   }
-  b = s_scan[0];
-  int64_t into = s_scan[1];
+  __syncthreads();
+  int b = s_scan[0];
+  const int into = s_scan[1];
   Span sp = span_of(a, b, C::COST, false);
-  int item = static_cast<int>(into / sp.line);
-  int at_line = static_cast<int>(into - static_cast<int64_t>(item) * sp.line);   // place within the item
+  int item = into / sp.line;
+  int at_line = into - item * sp.line;                 // place within the item
+  if (threadIdx.x == 0) {
+    // What the joining kernel needs of an item that this block continues and the one before began: the
+    // last block of it.  (An item begins, for that, at its first unit.)
+    Rec rec{b, item, -1};
+    if (at_line > C::COST) {
+      const int64_t unit0 = at - at_line + C::COST, before = total * (blockIdx.x - 1) / grid;
+      if (unit0 >= before) rec.last = static_cast<int>(((unit0 + sp.n) * grid - 1) / total);
+    }
+    a.recs[blockIdx.x] = rec;
+  }
 
   Worker<KIND, D, U16> w(a);
   w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
@@ -774,8 +797,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
     w.lo = max(sp.first, t0);
     w.hi = min(sp.len, t0 + take * kUnit);
     if (take > 0) {
-      w.load_q(head0, heads);
-      w.walk(max(t0, w.lo & ~15), warp);
+      w.walk(max(t0, w.lo & ~15), warp, head0, heads);
 
       // join the warps: head h's reference is the largest of theirs
       __syncthreads();
@@ -788,7 +810,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
           s_l[warp][2 * w.t + c] = w.l[c];
         }
       }
-      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop);
+      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop<KIND>);
 #pragma unroll
       for (int j = 0; j < C::NV; ++j)
 #pragma unroll
@@ -840,48 +862,18 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   }
 }
 
-// One block per (sequence, query head): joins the parts of a split item in order, and writes the
-// zeros of an empty sequence.
+// Joins the parts of split items, in order.  An item is cut where a block's share ends, so the second of
+// its blocks (x) stands for it; y counts its heads.
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, int cost, float lift) {
-  __shared__ int64_t s_sum[8];
+__global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   __shared__ float s_o[4][D], s_m[4], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
-  const int hk = hq / a.G, hg = hq - hk * a.G, hb = hg / kHeads, h = hg - hb * kHeads;
-  int64_t before = 0, all = 0;
-  for (int i = threadIdx.x; i < a.B; i += 128) {
-    const int n = span_of(a, i, cost, false).line;
-    all += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if (lane == 0) { s_sum[warp] = before; s_sum[4 + warp] = all; }
-  __syncthreads();
-  before = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-  all = s_sum[4] + s_sum[5] + s_sum[6] + s_sum[7];
-  const int per_seq = a.kv_heads * a.HB;
-  const int64_t total = all * per_seq;
-  const Span sp = span_of(a, b, cost, false);
-  const int n = sp.n;
-  const int64_t row = static_cast<int64_t>(b) * a.q_heads + hq;
-  if (n == 0) {
-    pdl_wait();                               // (every block: the call ends after both kernels)
-    for (int d = threadIdx.x; d < D / 2; d += 128) reinterpret_cast<uint32_t*>(a.out + row * D)[d] = 0u;
-    if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
-    return;
-  }
-  const int64_t start = before * per_seq + static_cast<int64_t>(hk * a.HB + hb) * sp.line + cost;   // its first unit
-  // block c of those with a share holds [total c / grid, total (c + 1) / grid) of the line
-  const int64_t grid = total < blocks ? total : blocks;
-  const int c0 = static_cast<int>(((start + 1) * grid - 1) / total);
-  const int c1 = static_cast<int>(((start + n) * grid - 1) / total);
   pdl_wait();
-  if (c0 == c1) return;                       // written whole
+  const Rec rec = a.recs[blockIdx.x];
+  const int hk = rec.item / a.HB, hb = rec.item - hk * a.HB, h = blockIdx.y;
+  if (rec.last < 0 || hb * kHeads + h >= a.G) return;
+  const int c0 = blockIdx.x - 1, c1 = rec.last;
+  const int64_t row = static_cast<int64_t>(rec.b) * a.q_heads + hk * a.G + hb * kHeads + h;
   constexpr int V = D / 32;
   float o[V], m = kLowest, l = 0.f;
 #pragma unroll
@@ -889,11 +881,14 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, int blocks, int
   for (int c = c0 + warp; c <= c1; c += 4) {
     const float* part = a.parts + static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * kHeads * (D + 2);
     const float pm = part[kHeads * D + h], pl = part[kHeads * D + kHeads + h];
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = part[h * D + lane + 32 * i];
     const float mn = fmaxf(m, pm), f = exp2_fast(m - mn), g = exp2_fast(pm - mn);
     m = mn;
     l = l * f + pl * g;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, part[h * D + lane + 32 * i] * g);
+    for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, v[i] * g);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
@@ -931,9 +926,10 @@ w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
     return W4_ERR_CUDA;
   kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
+  if (grid == 1) return W4_OK;                           // nothing is split
   const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
-  const unsigned rows = static_cast<unsigned>(a.B) * a.q_heads;
-  return launch_pdl(join_kernel<D>, dim3(rows), dim3(128), 0, s, a, grid, Cfg<KIND, D>::COST, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+  const dim3 joins(grid, a.G < kHeads ? a.G : kHeads);
+  return launch_pdl(join_kernel<D>, joins, dim3(128), 0, s, a, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 template <int KIND>

@@ -1,50 +1,479 @@
 // w4a8_linear: y = xs * (xq (s q)^T), 8-bit activation rows times 4-bit group-32 weights.
 //
-// Inside a group of 32 the products of int8 activations and int4 codes are summed exactly in
-// integers; a group's sum times its bf16 scale is accumulated in float32, and the row's scale is
-// applied once at the end.
+// Inside a group of 32 the products of int8 activations and int4 codes are summed exactly in integers by
+// one m16n8k32 product (16 weight rows, 8 tokens); a group's sum times its bf16 scale is accumulated in
+// float32, and the row's scale is applied once at the end.
+//   * A code word of layout L1 holds 8 consecutive elements.  Flipping the top bit of its nibbles makes
+//     them two's complement; masked in place (odd elements) or shifted up by 4 (even ones) they are bytes
+//     16 q, so a word becomes two operand registers in three operations, and no offset has to be taken
+//     back.  The activation side is put in the same order, even elements and odd ones.
+//   * The product starts from 0x4B400000, the bits of 1.5 * 2^23: |16 * sum| <= 2^19, so the integer
+//     result read as a float32 is that number plus the sum, exactly, and one subtraction converts it.
 //
-// First form: one warp per output, a lane per group (four dp4a pairs of a 16-byte code load and
-// two 16-byte activation loads).
+// Two kernels.  Few rows (M <= 32, and the rows fit in shared memory): bound by the weights' bytes, which
+// each warp streams through its own ring of stages (cp.async) with no block-wide wait; the rows lie in
+// shared memory as ready operands.  More rows: tiles of 128 weight rows by 16 to 64 tokens, 128 k a stage.
 #include "common.cuh"
 #include "entry.cuh"
 
 namespace w4 {
 namespace a8 {
 
-__global__ void __launch_bounds__(256)
-linear_kernel(const int8_t* __restrict__ xq, const float* __restrict__ xs, const uint32_t* __restrict__ codes,
-              const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int64_t M, int64_t N, int64_t K) {
-  const int lane = threadIdx.x & 31;
-  const int64_t out = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (out >= M * N) return;
-  const int64_t m = out / N, n = out - m * N;
-  const int64_t groups = K >> 5;
-  float acc = 0.f;
-  for (int64_t g = lane; g < groups; g += 32) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + n * (K >> 3)) + g);
-    const uint4* xr = reinterpret_cast<const uint4*>(xq + m * K) + 2 * g;
-    const uint4 x0 = __ldg(xr), x1 = __ldg(xr + 1);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    const uint32_t xx[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-    int sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // elements 0,2,4,6 and 1,3,5,7 of the word, times 16 as signed bytes
-      const int even = static_cast<int>(((ww[j] ^ 0x88888888u) << 4) & 0xF0F0F0F0u);
-      const int odd = static_cast<int>((ww[j] ^ 0x88888888u) & 0xF0F0F0F0u);
-      sum = __dp4a(even, static_cast<int>(__byte_perm(xx[2 * j], xx[2 * j + 1], 0x6420)), sum);
-      sum = __dp4a(odd, static_cast<int>(__byte_perm(xx[2 * j], xx[2 * j + 1], 0x7531)), sum);
+constexpr uint32_t kMagic = 0x4B400000u;
+constexpr float kMagicF = 12582912.f;
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+  const int n = on ? N : 0;                          // bytes read; the rest of the destination is zeroed
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 16 * q of the odd (even: after a shift by 4) elements of a code word
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(r) : "r"(w), "r"(0x80808080u), "r"(0xF0F0F0F0u));   // (a ^ b) & c
+  return r;
+}
+
+__device__ __forceinline__ void mma_s8(uint32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kMagic));
+}
+
+// acc (two neighbouring tokens) += s * (sums - magic), as packed float32 pairs
+__device__ __forceinline__ void add_scaled(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t ss) {
+  uint64_t v, m;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(d0), "r"(d1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(m) : "f"(-kMagicF));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(m));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(ss));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(s));
+  return v;
+}
+__device__ __forceinline__ void halves(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+struct Args {
+  const int8_t* x;
+  const float* xs;
+  const uint32_t* codes;
+  const uint16_t* scales;
+  uint16_t* y;
+  int64_t M, N;
+  int K, KG;                       // KG = K / 32 groups
+  float* parts;                    // [splits][M][N], when K is split over blocks
+};
+
+// ------------------------------------------------------------------------------------ few rows
+constexpr int kWarps = 8;
+constexpr int kUnitRows = 16, kUnitGroups = 8;           // a stage: 16 weight rows by 256 k
+constexpr int kRowPitch = 16 * kUnitGroups + 16;         // 9 chunks: a read of 8 rows covers all banks once
+constexpr int kStageBytes = kUnitRows * kRowPitch + kUnitRows * 2 * kUnitGroups;
+constexpr int kTilesPass = kWarps;                       // row tiles a block works on at once
+
+// NT blocks of 8 tokens.  SB: bytes a scale copy may take (16, 4 or 2, by the scales' alignment).
+// A block owns a run of weight rows (multiples of 8) in passes of up to 8 tiles of 16; a pass's tiles
+// times its stages form a line that the warps share evenly, so a tile is cut over two warps at most
+// times (its K is long) and their sums are joined in shared memory, in order.
+template <int NT, int SB>
+__global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
+  uint2* xf = reinterpret_cast<uint2*>(smem);                                  // [NT][8 KT][32] operands
+  uint8_t* rings = smem + static_cast<size_t>(NT) * KT * kUnitGroups * 256;
+  float* red = reinterpret_cast<float*>(rings + kWarps * S * kStageBytes);      // [kWarps][2][8 NT][16]
+  const uint32_t ring = smem_u32(rings) + warp * S * kStageBytes;
+
+  const int64_t R8 = (a.N + 7) / 8;
+  const int64_t row_begin = R8 * blockIdx.x / gridDim.x * 8;
+  const int64_t row_end = min(a.N, R8 * (blockIdx.x + 1) / gridDim.x * 8);
+  const int tiles = static_cast<int>((row_end - row_begin + kUnitRows - 1) / kUnitRows);
+  if (tiles <= 0) return;
+
+  // this warp's place in the sequence of (pass, tile, stage)
+  struct Place {
+    int pass, u, end;              // units of the pass: u counts tile * KT + stage
+  };
+  auto pass_tiles = [&](int p) { return min(kTilesPass, tiles - p * kTilesPass); };
+  auto enter = [&](Place& p) {     // skips passes that leave this warp nothing
+    for (; p.pass * kTilesPass < tiles; ++p.pass) {
+      const int U = pass_tiles(p.pass) * KT;
+      p.u = U * warp / kWarps;
+      p.end = U * (warp + 1) / kWarps;
+      if (p.u < p.end) return true;
     }
-    acc = fmaf(static_cast<float>(sum), bf16_lo_to_f32(__ldg(scales + n * groups + g)), acc);
-  }
+    return false;
+  };
+  auto fetch = [&](const Place& p, int st) {
+    const int tile = p.pass * kTilesPass + p.u / KT, kt = p.u % KT;
+    const int64_t row0 = row_begin + static_cast<int64_t>(tile) * kUnitRows;
+    const uint32_t base = ring + st * kStageBytes;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (lane == 0) y[out] = f32_to_bf16_bits(acc * 0.0625f * __ldg(xs + m));
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * i + (lane >> 3), col = lane & 7, g = kt * kUnitGroups + col;
+      const bool on = row0 + row < row_end && g < a.KG;
+      const uint32_t* src = a.codes + (on ? (row0 + row) * (a.K >> 3) + g * 4 : 0);
+      copy_async<16>(base + row * kRowPitch + col * 16, src, on);
+    }
+    const uint32_t sb = base + kUnitRows * kRowPitch;
+    if constexpr (SB == 16) {
+      if (lane < 16) {
+        const bool on = row0 + lane < row_end;
+        copy_async<16>(sb + lane * 16, a.scales + (on ? (row0 + lane) * a.KG + kt * kUnitGroups : 0), on);
+      }
+    } else if constexpr (SB == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + (lane >> 2), g = kt * kUnitGroups + 2 * (lane & 3);
+        const bool on = row0 + row < row_end && g < a.KG;
+        copy_async<4>(sb + row * 16 + (lane & 3) * 4, a.scales + (on ? (row0 + row) * a.KG + g : 0), on);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + (lane >> 3), g = kt * kUnitGroups + (lane & 7);
+        const bool on = row0 + row < row_end && g < a.KG;
+        const uint16_t v = on ? ldg_u16(a.scales + (row0 + row) * a.KG + g) : 0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(sb + row * 16 + (lane & 7) * 2), "h"(v) : "memory");
+      }
+    }
+  };
+
+  Place at{0, 0, 0}, ahead;
+  bool have = enter(at);
+  ahead = at;
+  bool more = have;
+  auto advance = [&](Place& p) {
+    if (++p.u < p.end) return true;
+    ++p.pass;
+    return enter(p);
+  };
+  int filled = 0;
+  for (; filled < S - 1; ++filled) {
+    if (more) {
+      fetch(ahead, filled);
+      more = advance(ahead);
+    }
+    copy_commit();
+  }
+
+  // the rows as operands, while the first stages are on their way: lane (r, t) of token block b, group g
+  // holds the even and the odd ones of elements 32 g + 8 t .. + 7 of token 8 b + r
+  for (int i = threadIdx.x; i < NT * KT * kUnitGroups * 32; i += 32 * kWarps) {
+    const int l = i & 31, gb = i >> 5, g = gb % (KT * kUnitGroups), b = gb / (KT * kUnitGroups);
+    const int64_t m = b * 8 + (l >> 2);
+    uint2 v = make_uint2(0, 0);
+    if (m < a.M && g < a.KG) v = __ldg(reinterpret_cast<const uint2*>(a.x + m * a.K + g * 32 + (l & 3) * 8));
+    xf[i] = make_uint2(__byte_perm(v.x, v.y, 0x6420), __byte_perm(v.x, v.y, 0x7531));
+  }
+  __syncthreads();
+
+  uint64_t acc[NT][2];
+#pragma unroll
+  for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = 0;
+  int st = 0, into = S - 1;
+  const uint32_t xbase = smem_u32(xf) + lane * 8;
+  for (int pass = 0; pass * kTilesPass < tiles; ++pass) {
+    const int U = pass_tiles(pass) * KT;
+    int slot = 0;
+    if (have && at.pass == pass) {
+      while (true) {
+        // S is a run-time number: leave S - 2 groups in flight
+        if (S == 3) copy_wait<1>();
+        else if (S == 4) copy_wait<2>();
+        else if (S == 5) copy_wait<3>();
+        else copy_wait<4>();
+        __syncwarp();
+        if (more) {
+          fetch(ahead, into);
+          more = advance(ahead);
+        }
+        copy_commit();
+        const uint32_t base = ring + st * kStageBytes;
+        const int kt = at.u % KT;
+        const uint4 s0 = lds128(base + kUnitRows * kRowPitch + r * 16), s1 = lds128(base + kUnitRows * kRowPitch + (r + 8) * 16);
+        const uint32_t sw[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
+#pragma unroll
+        for (int g = 0; g < kUnitGroups; ++g) {
+          const uint32_t w0 = lds32(base + r * kRowPitch + g * 16 + t * 4), w1 = lds32(base + (r + 8) * kRowPitch + g * 16 + t * 4);
+          const uint32_t a0 = codes_hi(w0 << 4), a1 = codes_hi(w1 << 4), a2 = codes_hi(w0), a3 = codes_hi(w1);
+          const uint64_t q0 = twice(g & 1 ? bf16_hi_to_f32(sw[0][g / 2]) : bf16_lo_to_f32(sw[0][g / 2]));
+          const uint64_t q1 = twice(g & 1 ? bf16_hi_to_f32(sw[1][g / 2]) : bf16_lo_to_f32(sw[1][g / 2]));
+#pragma unroll
+          for (int b = 0; b < NT; ++b) {
+            const uint2 x = lds64(xbase + ((b * KT + kt) * kUnitGroups + g) * 256);
+            uint32_t d[4];
+            mma_s8(d, a0, a1, a2, a3, x.x, x.y);
+            add_scaled(acc[b][0], d[0], d[1], q0);
+            add_scaled(acc[b][1], d[2], d[3], q1);
+          }
+        }
+        into = st;
+        st = st + 1 == S ? 0 : st + 1;
+        const int tile = at.u / KT;
+        const bool go_on = advance(at);
+        have = go_on;
+        if (!go_on || at.pass != pass || at.u / KT != tile) {
+          float* o = red + (warp * 2 + slot) * (8 * NT * 16);        // [token][row]
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float lo, hi;
+              halves(acc[b][h], lo, hi);
+              o[(8 * b + 2 * t) * 16 + r + 8 * h] = lo;
+              o[(8 * b + 2 * t + 1) * 16 + r + 8 * h] = hi;
+              acc[b][h] = 0;
+            }
+          ++slot;
+          if (!go_on || at.pass != pass) break;
+        }
+      }
+    }
+    __syncthreads();
+    // tile by tile: the sums of the warps that hold a part of it, in order
+    for (int i = threadIdx.x; i < pass_tiles(pass) * 16 * 8 * NT; i += 32 * kWarps) {
+      const int row = i & 15, tile = (i >> 4) % pass_tiles(pass), m = (i >> 4) / pass_tiles(pass);
+      const int64_t n = row_begin + static_cast<int64_t>(pass * kTilesPass + tile) * kUnitRows + row;
+      if (m >= a.M || n >= row_end) continue;
+      const int u0 = tile * KT, u1 = u0 + KT;
+      float sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) {
+        const int b0 = U * w / kWarps, b1 = U * (w + 1) / kWarps;
+        if (b0 < u1 && b1 > u0 && b0 < b1) sum += red[((w * 2 + (tile - b0 / KT)) * 8 * NT + m) * 16 + row];
+      }
+      a.y[m * a.N + n] = f32_to_bf16_bits(sum * 0.0625f * __ldg(a.xs + m));
+    }
+    __syncthreads();
+  }
+  copy_wait<0>();
+}
+
+// ----------------------------------------------------------------------------------- more rows
+constexpr int kBN = 128, kGS = 4;                        // weight rows of a tile, groups a stage (128 k)
+constexpr int kWPitch = 16 * kGS + 16, kXPitch = 32 * kGS + 32;
+constexpr int kManyStages = 4;
+
+template <int BM>
+struct Many {
+  static constexpr int WR = BM >= 64 ? 4 : 8, WC = 8 / WR;         // warps over rows, over tokens
+  static constexpr int MT = kBN / 16 / WR, NT = BM / 8 / WC;       // 16-row and 8-token blocks of a warp
+  static constexpr int kScales = kBN * kWPitch, kX = kScales + kBN * 2 * kGS;
+  static constexpr int kStage = kX + BM * kXPitch;
+  static constexpr int kOut = BM * (kBN + 4) * 4;
+  static constexpr int kSmem = kManyStages * kStage > kOut ? kManyStages * kStage : kOut;
+};
+
+// blockIdx.x: token tile (fastest, so that a weight tile is shared in L2), y: row tile, z: part of K.
+template <int BM, int SB>
+__global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
+  using C = Many<BM>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  const int wr = warp % C::WR, wc = warp / C::WR;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * BM, n0 = static_cast<int64_t>(blockIdx.y) * kBN;
+  const int KT = (a.KG + kGS - 1) / kGS;
+  const int k0 = static_cast<int>(static_cast<int64_t>(KT) * blockIdx.z / gridDim.z);
+  const int k1 = static_cast<int>(static_cast<int64_t>(KT) * (blockIdx.z + 1) / gridDim.z);
+  const uint32_t s0 = smem_u32(smem);
+
+  auto fetch = [&](int kt, int st) {
+    const uint32_t base = s0 + st * C::kStage;
+#pragma unroll
+    for (int i = 0; i < kBN * kGS / 256; ++i) {
+      const int c = i * 256 + threadIdx.x, row = c / kGS, g = kt * kGS + c % kGS;
+      const bool on = n0 + row < a.N && g < a.KG;
+      copy_async<16>(base + row * kWPitch + (c % kGS) * 16, a.codes + (on ? (n0 + row) * (a.K >> 3) + g * 4 : 0), on);
+    }
+    if constexpr (SB >= 8) {
+      if (threadIdx.x < kBN) {
+        const int row = threadIdx.x;
+        const bool on = n0 + row < a.N;
+        copy_async<8>(base + C::kScales + row * 8, a.scales + (on ? (n0 + row) * a.KG + kt * kGS : 0), on);
+      }
+    } else if constexpr (SB == 4) {
+      const int row = threadIdx.x >> 1, g = kt * kGS + 2 * (threadIdx.x & 1);
+      const bool on = n0 + row < a.N && g < a.KG;
+      copy_async<4>(base + C::kScales + threadIdx.x * 4, a.scales + (on ? (n0 + row) * a.KG + g : 0), on);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = i * 256 + threadIdx.x, row = c / kGS, g = kt * kGS + c % kGS;
+        const uint16_t v = n0 + row < a.N && g < a.KG ? ldg_u16(a.scales + (n0 + row) * a.KG + g) : 0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + C::kScales + c * 2), "h"(v) : "memory");
+      }
+    }
+    for (int c = threadIdx.x; c < BM * 2 * kGS; c += 256) {
+      const int row = c / (2 * kGS), col = c % (2 * kGS), k = kt * kGS * 32 + col * 16;
+      const bool on = m0 + row < a.M && k < a.K;
+      copy_async<16>(base + C::kX + row * kXPitch + col * 16, a.x + (on ? (m0 + row) * a.K + k : 0), on);
+    }
+  };
+
+  uint64_t acc[C::MT][C::NT][2];
+#pragma unroll
+  for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j) acc[i][j][0] = acc[i][j][1] = 0;
+
+  for (int i = 0; i < kManyStages - 1; ++i) {
+    if (k0 + i < k1) fetch(k0 + i, i);
+    copy_commit();
+  }
+  int st = 0;
+  for (int kt = k0; kt < k1; ++kt) {
+    copy_wait<kManyStages - 2>();
+    __syncthreads();
+    if (kt + kManyStages - 1 < k1) fetch(kt + kManyStages - 1, (st + kManyStages - 1) % kManyStages);
+    copy_commit();
+    const uint32_t base = s0 + st * C::kStage;
+    const uint32_t wb = base + (wr * C::MT * 16 + r) * kWPitch + t * 4;
+    const uint32_t xb = base + C::kX + (wc * C::NT * 8 + r) * kXPitch + t * 8;
+    uint2 sw[C::MT][2];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sw[i][h] = lds64(base + C::kScales + (wr * C::MT * 16 + i * 16 + h * 8 + r) * 8);
+#pragma unroll
+    for (int g = 0; g < kGS; ++g) {
+      uint32_t xe[C::NT], xo[C::NT];
+#pragma unroll
+      for (int j = 0; j < C::NT; ++j) {
+        const uint2 x = lds64(xb + j * 8 * kXPitch + g * 32);
+        xe[j] = __byte_perm(x.x, x.y, 0x6420);
+        xo[j] = __byte_perm(x.x, x.y, 0x7531);
+      }
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i) {
+        const uint32_t w0 = lds32(wb + i * 16 * kWPitch + g * 16), w1 = lds32(wb + (i * 16 + 8) * kWPitch + g * 16);
+        const uint32_t a0 = codes_hi(w0 << 4), a1 = codes_hi(w1 << 4), a2 = codes_hi(w0), a3 = codes_hi(w1);
+        const uint32_t p0 = g < 2 ? sw[i][0].x : sw[i][0].y, p1 = g < 2 ? sw[i][1].x : sw[i][1].y;
+        const uint64_t q0 = twice(g & 1 ? bf16_hi_to_f32(p0) : bf16_lo_to_f32(p0));
+        const uint64_t q1 = twice(g & 1 ? bf16_hi_to_f32(p1) : bf16_lo_to_f32(p1));
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j) {
+          uint32_t d[4];
+          mma_s8(d, a0, a1, a2, a3, xe[j], xo[j]);
+          add_scaled(acc[i][j][0], d[0], d[1], q0);
+          add_scaled(acc[i][j][1], d[2], d[3], q1);
+        }
+      }
+    }
+    st = st + 1 == kManyStages ? 0 : st + 1;
+  }
+  copy_wait<0>();
+  __syncthreads();
+  float* o = reinterpret_cast<float*>(smem);               // [token][kBN + 4]
+#pragma unroll
+  for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float lo, hi;
+        halves(acc[i][j][h], lo, hi);
+        const int m = wc * C::NT * 8 + j * 8 + 2 * t, n = wr * C::MT * 16 + i * 16 + h * 8 + r;
+        o[m * (kBN + 4) + n] = lo;
+        o[(m + 1) * (kBN + 4) + n] = hi;
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < BM * kBN; i += 256) {
+    const int m = i / kBN, n = i % kBN;
+    if (m0 + m >= a.M || n0 + n >= a.N) continue;
+    const float v = o[m * (kBN + 4) + n];
+    if (gridDim.z > 1) a.parts[(blockIdx.z * a.M + m0 + m) * a.N + n0 + n] = v;
+    else a.y[(m0 + m) * a.N + n0 + n] = f32_to_bf16_bits(v * 0.0625f * __ldg(a.xs + m0 + m));
+  }
+}
+
+// sums the parts of a split K in order
+__global__ void __launch_bounds__(256) parts_kernel(const Args a, int splits) {
+  pdl_wait();
+  const int64_t total = a.M * a.N;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    float v = 0.f;
+    for (int z = 0; z < splits; ++z) v += a.parts[z * total + i];
+    a.y[i] = f32_to_bf16_bits(v * 0.0625f * __ldg(a.xs + i / a.N));
+  }
+}
+
+// ----------------------------------------------------------------------------------- dispatch
+constexpr int kSmemMost = 232448;
+
+// Stages of the few-rows kernel for NT token blocks; 0 where the rows leave no room for three.
+int few_stages(int64_t M, int64_t KG, int& NT) {
+  if (M > 32) return 0;
+  NT = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+  const int64_t KT = (KG + kUnitGroups - 1) / kUnitGroups;
+  const int64_t left = kSmemMost - NT * KT * kUnitGroups * 256 - kWarps * 2 * 8 * NT * 16 * 4;
+  const int64_t S = left / (kWarps * kStageBytes);
+  return S < 3 ? 0 : S > 6 ? 6 : static_cast<int>(S);
+}
+
+int many_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+// Parts of K: enough to give every SM a block, each at least 1024 k long
+int many_splits(int64_t M, int64_t N, int64_t KG, int sms) {
+  const int BM = many_tile(M);
+  const int64_t tiles = (M + BM - 1) / BM * ((N + kBN - 1) / kBN);
+  const int64_t want = sms / tiles, most = KG / 32;
+  const int64_t s = want < most ? want : most;
+  return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
+}
+
+template <typename F>
+cudaError_t raise_smem(F* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int NT>
+w4_status launch_few(const Args& a, int S, int SB, int sms, cudaStream_t s) {
+  auto kernel = SB == 16 ? few_kernel<NT, 16> : SB >= 4 ? few_kernel<NT, 4> : few_kernel<NT, 2>;
+  const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
+  const int smem = NT * KT * kUnitGroups * 256 + kWarps * S * kStageBytes + kWarps * 2 * 8 * NT * 16 * 4;
+  if (raise_smem(kernel, smem) != cudaSuccess) return W4_ERR_CUDA;
+  const int64_t R8 = (a.N + 7) / 8;
+  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * kWarps, smem, s>>>(a, S);
+  return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int BM>
+w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s) {
+  auto kernel = SB >= 8 ? many_kernel<BM, 8> : SB == 4 ? many_kernel<BM, 4> : many_kernel<BM, 2>;
+  if (raise_smem(kernel, Many<BM>::kSmem) != cudaSuccess) return W4_ERR_CUDA;
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + kBN - 1) / kBN;
+  if (tm > 0x7FFFFFFFLL || tn > 65535) return W4_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(tm), static_cast<unsigned>(tn), splits);
+  kernel<<<grid, 256, Many<BM>::kSmem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
+  if (splits == 1) return W4_OK;
+  const int64_t blocks = (a.M * a.N + 255) / 256;
+  return launch_pdl(parts_kernel, dim3(static_cast<unsigned>(blocks < 4 * sms ? blocks : 4 * sms)), dim3(256), 0, s, a,
+                    splits) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 }  // namespace a8
 }  // namespace w4
+
+size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 32 || K % 32) return 0;
+  int NT;
+  if (w4::a8::few_stages(M, K / 32, NT)) return 0;
+  const int splits = w4::a8::many_splits(M, N, K / 32, w4::device_sm_count());
+  return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+}
 
 extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
                                  uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -58,14 +487,22 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
     return W4_ERR_INVALID_ARG;
   if (M > (1LL << 40) / N) return W4_ERR_UNSUPPORTED;
   if (M == 0) return W4_OK;
-  if (workspace_bytes < w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1) ||
-      (!workspace && w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1)))
-    return W4_ERR_WORKSPACE;
-  const int64_t blocks = (M * N + 7) / 8;
-  if (blocks > 0x7FFFFFFFLL) return W4_ERR_UNSUPPORTED;
-  a8::linear_kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(xq, xs, codes,
-                                                                                               scales, y, M, N, K);
-  return launched();
+  const size_t need = w4_linear8_workspace_bytes(M, N, K);
+  if (need && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
+  a8::Args a{xq, xs, codes, scales, y, M, N, static_cast<int>(K), static_cast<int>(K / 32), static_cast<float*>(workspace)};
+  auto s = static_cast<cudaStream_t>(stream);
+  const int sms = device_sm_count();
+  // what a copy of consecutive scales may take at once: every row starts at a multiple of it
+  const int SB = K % 256 == 0 && aligned_to(scales, 16) ? 16
+                 : K % 128 == 0 && aligned_to(scales, 8) ? 8
+                 : K % 64 == 0 && aligned_to(scales, 4) ? 4 : 2;
+  int NT;
+  if (const int S = a8::few_stages(M, K / 32, NT))
+    return w4_record_status(NT == 1 ? a8::launch_few<1>(a, S, SB, sms, s)
+                            : NT == 2 ? a8::launch_few<2>(a, S, SB, sms, s) : a8::launch_few<4>(a, S, SB, sms, s));
+  const int splits = a8::many_splits(M, N, K / 32, sms);
+  const int BM = a8::many_tile(M);
+  return w4_record_status(BM == 16 ? a8::launch_many<16>(a, splits, SB, sms, s)
+                          : BM == 32 ? a8::launch_many<32>(a, splits, SB, sms, s)
+                                     : a8::launch_many<64>(a, splits, SB, sms, s));
 }
-
-size_t w4_linear8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }

@@ -76,24 +76,25 @@ struct Args {
 };
 
 // ------------------------------------------------------------------------------------ few rows
-constexpr int kWarps = 8;
 constexpr int kUnitRows = 16, kUnitGroups = 8;           // a stage: 16 weight rows by 256 k
 constexpr int kRowPitch = 16 * kUnitGroups + 16;         // 9 chunks: a read of 8 rows covers all banks once
 constexpr int kStageBytes = kUnitRows * kRowPitch + kUnitRows * 2 * kUnitGroups;
-constexpr int kTilesPass = kWarps;                       // row tiles a block works on at once
 
-// NT blocks of 8 tokens.  SB: bytes a scale copy may take (16, 4 or 2, by the scales' alignment).
-// A block owns a run of weight rows (multiples of 8) in passes of up to 8 tiles of 16; a pass's tiles
+// W warps, NT blocks of 8 tokens.  SB: bytes a scale copy may take (16, 4 or 2, by the scales' alignment).
+// A block owns a run of weight rows (multiples of 8) in passes of up to W tiles of 16; a pass's tiles
 // times its stages form a line that the warps share evenly, so a tile is cut over two warps at most
 // times (its K is long) and their sums are joined in shared memory, in order.
-template <int NT, int SB>
-__global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S) {
+template <int W, int NT, int SB>
+__global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
   uint2* xf = reinterpret_cast<uint2*>(smem);                                  // [NT][8 KT][32] operands
   uint8_t* rings = smem + static_cast<size_t>(NT) * KT * kUnitGroups * 256;
-  float* red = reinterpret_cast<float*>(rings + kWarps * S * kStageBytes);      // [kWarps][2][8 NT][16]
+  // sums of the parts of a pass's tiles: the part that warp w has of a tile lies at w + tile, so a tile's
+  // parts follow one another in the order of their stages
+  float* red = reinterpret_cast<float*>(rings + W * S * kStageBytes);          // [2 W][8 NT][16]
+  __shared__ int s_first[W], s_last[W];                                        // a tile's first and last warp
   const uint32_t ring = smem_u32(rings) + warp * S * kStageBytes;
 
   const int64_t R8 = (a.N + 7) / 8;
@@ -104,28 +105,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
 
   // this warp's place in the sequence of (pass, tile, stage)
   struct Place {
-    int pass, u, end;              // units of the pass: u counts tile * KT + stage
+    int pass, tile, kt, left;      // tile of the pass, its stage, units left to this warp in the pass
   };
-  auto pass_tiles = [&](int p) { return min(kTilesPass, tiles - p * kTilesPass); };
+  auto pass_tiles = [&](int p) { return min(W, tiles - p * W); };
   auto enter = [&](Place& p) {     // skips passes that leave this warp nothing
-    for (; p.pass * kTilesPass < tiles; ++p.pass) {
-      const int U = pass_tiles(p.pass) * KT;
-      p.u = U * warp / kWarps;
-      p.end = U * (warp + 1) / kWarps;
-      if (p.u < p.end) return true;
+    for (; p.pass * W < tiles; ++p.pass) {
+      const int U = pass_tiles(p.pass) * KT, u = U < W ? min(warp, U) : U * warp / W;
+      p.left = (U < W ? min(warp + 1, U) : U * (warp + 1) / W) - u;
+      p.tile = u / KT;
+      p.kt = u - p.tile * KT;
+      if (p.left > 0) return true;
     }
     return false;
   };
+  const uint32_t* lane_codes = a.codes + (row_begin + (lane >> 3)) * (a.K >> 3) + (lane & 7) * 4;
   auto fetch = [&](const Place& p, int st) {
-    const int tile = p.pass * kTilesPass + p.u / KT, kt = p.u % KT;
-    const int64_t row0 = row_begin + static_cast<int64_t>(tile) * kUnitRows;
+    const int kt = p.kt, tile16 = (p.pass * W + p.tile) * kUnitRows;
+    const int64_t row0 = row_begin + tile16;
     const uint32_t base = ring + st * kStageBytes;
+    const int rows = static_cast<int>(min(row_end - row0, static_cast<int64_t>(kUnitRows))) - (lane >> 3);
+    const uint32_t* src = lane_codes + static_cast<int64_t>(tile16) * (a.K >> 3) + kt * (4 * kUnitGroups);
+    const uint32_t dst = base + (lane >> 3) * kRowPitch + (lane & 7) * 16;
+    const bool in_k = kt * kUnitGroups + (lane & 7) < a.KG;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 4 * i + (lane >> 3), col = lane & 7, g = kt * kUnitGroups + col;
-      const bool on = row0 + row < row_end && g < a.KG;
-      const uint32_t* src = a.codes + (on ? (row0 + row) * (a.K >> 3) + g * 4 : 0);
-      copy_async<16>(base + row * kRowPitch + col * 16, src, on);
+      const bool on = in_k && 4 * i < rows;
+      copy_async<16>(dst + 4 * i * kRowPitch, on ? src + static_cast<int64_t>(4 * i) * (a.K >> 3) : a.codes, on);
     }
     const uint32_t sb = base + kUnitRows * kRowPitch;
     if constexpr (SB == 16) {
@@ -151,12 +156,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
     }
   };
 
-  Place at{0, 0, 0}, ahead;
+  Place at{0, 0, 0, 0}, ahead;
   bool have = enter(at);
   ahead = at;
   bool more = have;
   auto advance = [&](Place& p) {
-    if (++p.u < p.end) return true;
+    if (--p.left > 0) {
+      if (++p.kt == KT) {
+        p.kt = 0;
+        ++p.tile;
+      }
+      return true;
+    }
     ++p.pass;
     return enter(p);
   };
@@ -171,12 +182,28 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
 
   // the rows as operands, while the first stages are on their way: lane (r, t) of token block b, group g
   // holds the even and the odd ones of elements 32 g + 8 t .. + 7 of token 8 b + r
-  for (int i = threadIdx.x; i < NT * KT * kUnitGroups * 32; i += 32 * kWarps) {
-    const int l = i & 31, gb = i >> 5, g = gb % (KT * kUnitGroups), b = gb / (KT * kUnitGroups);
-    const int64_t m = b * 8 + (l >> 2);
-    uint2 v = make_uint2(0, 0);
-    if (m < a.M && g < a.KG) v = __ldg(reinterpret_cast<const uint2*>(a.x + m * a.K + g * 32 + (l & 3) * 8));
-    xf[i] = make_uint2(__byte_perm(v.x, v.y, 0x6420), __byte_perm(v.x, v.y, 0x7531));
+  constexpr int kBatch = 16 / NT;                      // 16 loads in flight a lane
+  for (int g0 = warp; g0 < KT * kUnitGroups; g0 += W * kBatch) {
+    uint2 v[NT][kBatch];
+#pragma unroll
+    for (int b = 0; b < NT; ++b) {
+      const int64_t m = b * 8 + r;
+      const int8_t* row = a.x + (m < a.M ? m : 0) * a.K + t * 8;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i * W;
+        v[b][i] = m < a.M && g < a.KG ? __ldg(reinterpret_cast<const uint2*>(row + g * 32)) : make_uint2(0, 0);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i * W;
+        if (g < KT * kUnitGroups)
+          xf[(b * KT * kUnitGroups + g) * 32 + lane] = make_uint2(__byte_perm(v[b][i].x, v[b][i].y, 0x6420),
+                                                                  __byte_perm(v[b][i].x, v[b][i].y, 0x7531));
+      }
   }
   __syncthreads();
 
@@ -185,10 +212,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
   for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = 0;
   int st = 0, into = S - 1;
   const uint32_t xbase = smem_u32(xf) + lane * 8;
-  for (int pass = 0; pass * kTilesPass < tiles; ++pass) {
-    const int U = pass_tiles(pass) * KT;
-    int slot = 0;
+  for (int pass = 0; pass * W < tiles; ++pass) {
     if (have && at.pass == pass) {
+      bool first = at.kt == 0;
       while (true) {
         // S is a run-time number: leave S - 2 groups in flight
         if (S == 3) copy_wait<1>();
@@ -202,7 +228,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
         }
         copy_commit();
         const uint32_t base = ring + st * kStageBytes;
-        const int kt = at.u % KT;
+        const int kt = at.kt;
         const uint4 s0 = lds128(base + kUnitRows * kRowPitch + r * 16), s1 = lds128(base + kUnitRows * kRowPitch + (r + 8) * 16);
         const uint32_t sw[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
 #pragma unroll
@@ -222,11 +248,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
         }
         into = st;
         st = st + 1 == S ? 0 : st + 1;
-        const int tile = at.u / KT;
-        const bool go_on = advance(at);
-        have = go_on;
-        if (!go_on || at.pass != pass || at.u / KT != tile) {
-          float* o = red + (warp * 2 + slot) * (8 * NT * 16);        // [token][row]
+        const int tile = at.tile;
+        const bool last = kt == KT - 1;
+        have = advance(at);
+        if (!have || at.pass != pass || last) {
+          float* o = red + (warp + tile) * (8 * NT * 16);            // [token][row]
 #pragma unroll
           for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -237,24 +263,38 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_kernel(const Args a, int S
               o[(8 * b + 2 * t + 1) * 16 + r + 8 * h] = hi;
               acc[b][h] = 0;
             }
-          ++slot;
-          if (!go_on || at.pass != pass) break;
+          if (lane == 0 && first) s_first[tile] = warp;
+          if (lane == 0 && last) s_last[tile] = warp;
+          first = true;
+          if (!have || at.pass != pass) break;
         }
       }
     }
     __syncthreads();
-    // tile by tile: the sums of the warps that hold a part of it, in order
-    for (int i = threadIdx.x; i < pass_tiles(pass) * 16 * 8 * NT; i += 32 * kWarps) {
-      const int row = i & 15, tile = (i >> 4) % pass_tiles(pass), m = (i >> 4) / pass_tiles(pass);
-      const int64_t n = row_begin + static_cast<int64_t>(pass * kTilesPass + tile) * kUnitRows + row;
+    // a thread sums 4 rows of a token over the tile's parts, in order
+    for (int i = threadIdx.x; i < pass_tiles(pass) * 32 * NT; i += 32 * W) {
+      const int quad = i & 3, m = (i >> 2) % (8 * NT), tile = (i >> 2) / (8 * NT);
+      const int64_t n = row_begin + (pass * W + tile) * kUnitRows + quad * 4;
       if (m >= a.M || n >= row_end) continue;
-      const int u0 = tile * KT, u1 = u0 + KT;
-      float sum = 0.f;
-      for (int w = 0; w < kWarps; ++w) {
-        const int b0 = U * w / kWarps, b1 = U * (w + 1) / kWarps;
-        if (b0 < u1 && b1 > u0 && b0 < b1) sum += red[((w * 2 + (tile - b0 / KT)) * 8 * NT + m) * 16 + row];
+      const float4* part = reinterpret_cast<const float4*>(red) + ((s_first[tile] + tile) * 8 * NT + m) * 4 + quad;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = s_first[tile]; w <= s_last[tile]; ++w, part += 8 * NT * 4) {
+        sum.x += part->x;
+        sum.y += part->y;
+        sum.z += part->z;
+        sum.w += part->w;
       }
-      a.y[m * a.N + n] = f32_to_bf16_bits(sum * 0.0625f * __ldg(a.xs + m));
+      const float f = 0.0625f * __ldg(a.xs + m);
+      const uint2 o = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+      uint16_t* y = a.y + m * a.N + n;
+      if (a.N % 4 == 0) {
+        *reinterpret_cast<uint2*>(y) = o;
+      } else {
+        const uint16_t h[4] = {static_cast<uint16_t>(o.x), static_cast<uint16_t>(o.x >> 16), static_cast<uint16_t>(o.y),
+                               static_cast<uint16_t>(o.y >> 16)};
+        for (int q = 0; q < 4; ++q)
+          if (n + q < row_end) y[q] = h[q];
+      }
     }
     __syncthreads();
   }
@@ -412,14 +452,24 @@ __global__ void __launch_bounds__(256) parts_kernel(const Args a, int splits) {
 // ----------------------------------------------------------------------------------- dispatch
 constexpr int kSmemMost = 232448;
 
-// Stages of the few-rows kernel for NT token blocks; 0 where the rows leave no room for three.
-int few_stages(int64_t M, int64_t KG, int& NT) {
-  if (M > 32) return 0;
-  NT = M <= 8 ? 1 : M <= 16 ? 2 : 4;
-  const int64_t KT = (KG + kUnitGroups - 1) / kUnitGroups;
-  const int64_t left = kSmemMost - NT * KT * kUnitGroups * 256 - kWarps * 2 * 8 * NT * 16 * 4;
-  const int64_t S = left / (kWarps * kStageBytes);
-  return S < 3 ? 0 : S > 6 ? 6 : static_cast<int>(S);
+// How the few-rows kernel is run: W warps, NT token blocks, S stages; S = 0 where the rows leave no room.
+// 16 warps hide the latency of a warp's chain of products better (M 16, N 14336, K 4096: FIG16 us against
+// FIG8 us with 8), where their rings fit.
+struct Few {
+  int W, NT, S, smem;
+};
+Few few_plan(int64_t M, int64_t KG) {
+  Few f{16, M <= 8 ? 1 : M <= 16 ? 2 : 4, 0, 0};
+  if (M > 32) return f;
+  const int64_t x = f.NT * ((KG + kUnitGroups - 1) / kUnitGroups) * kUnitGroups * 256;
+  for (f.W = 16; f.W >= 8; f.W -= 8) {
+    const int64_t red = f.W * 2 * 8 * f.NT * 16 * 4, S = (kSmemMost - x - red) / (f.W * kStageBytes);
+    if (S < 3) continue;
+    f.S = S > 6 ? 6 : static_cast<int>(S);
+    f.smem = static_cast<int>(x + red + f.W * f.S * kStageBytes);
+    return f;
+  }
+  return f;
 }
 
 int many_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
@@ -438,15 +488,19 @@ cudaError_t raise_smem(F* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int NT>
-w4_status launch_few(const Args& a, int S, int SB, int sms, cudaStream_t s) {
-  auto kernel = SB == 16 ? few_kernel<NT, 16> : SB >= 4 ? few_kernel<NT, 4> : few_kernel<NT, 2>;
-  const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
-  const int smem = NT * KT * kUnitGroups * 256 + kWarps * S * kStageBytes + kWarps * 2 * 8 * NT * 16 * 4;
-  if (raise_smem(kernel, smem) != cudaSuccess) return W4_ERR_CUDA;
+template <int W, int NT>
+w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t s) {
+  auto kernel = SB == 16 ? few_kernel<W, NT, 16> : SB >= 4 ? few_kernel<W, NT, 4> : few_kernel<W, NT, 2>;
+  if (raise_smem(kernel, f.smem) != cudaSuccess) return W4_ERR_CUDA;
   const int64_t R8 = (a.N + 7) / 8;
-  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * kWarps, smem, s>>>(a, S);
+  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * W, f.smem, s>>>(a, f.S);
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int W>
+w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t s) {
+  return f.NT == 1 ? launch_few<W, 1>(a, f, SB, sms, s)
+         : f.NT == 2 ? launch_few<W, 2>(a, f, SB, sms, s) : launch_few<W, 4>(a, f, SB, sms, s);
 }
 
 template <int BM>
@@ -469,8 +523,7 @@ w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s
 
 size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 32 || K % 32) return 0;
-  int NT;
-  if (w4::a8::few_stages(M, K / 32, NT)) return 0;
+  if (w4::a8::few_plan(M, K / 32).S) return 0;
   const int splits = w4::a8::many_splits(M, N, K / 32, w4::device_sm_count());
   return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
 }
@@ -496,10 +549,9 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   const int SB = K % 256 == 0 && aligned_to(scales, 16) ? 16
                  : K % 128 == 0 && aligned_to(scales, 8) ? 8
                  : K % 64 == 0 && aligned_to(scales, 4) ? 4 : 2;
-  int NT;
-  if (const int S = a8::few_stages(M, K / 32, NT))
-    return w4_record_status(NT == 1 ? a8::launch_few<1>(a, S, SB, sms, s)
-                            : NT == 2 ? a8::launch_few<2>(a, S, SB, sms, s) : a8::launch_few<4>(a, S, SB, sms, s));
+  const a8::Few f = a8::few_plan(M, K / 32);
+  if (f.S)
+    return w4_record_status(f.W == 16 ? a8::launch_few<16>(a, f, SB, sms, s) : a8::launch_few<8>(a, f, SB, sms, s));
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);
   return w4_record_status(BM == 16 ? a8::launch_many<16>(a, splits, SB, sms, s)

@@ -11,8 +11,11 @@
 //     result read as a float32 is that number plus the sum, exactly, and one subtraction converts it.
 //
 // Two kernels.  Few rows (M <= 32, and the rows fit in shared memory): bound by the weights' bytes, which
-// each warp streams through its own ring of stages (cp.async) with no block-wide wait; the rows lie in
+// each warp streams through its own ring of stages (TMA tiles) with no block-wide wait; the rows lie in
 // shared memory as ready operands.  More rows: tiles of 128 weight rows by 16 to 64 tokens, 128 k a stage.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "entry.cuh"
 
@@ -77,25 +80,32 @@ struct Args {
 
 // ------------------------------------------------------------------------------------ few rows
 constexpr int kUnitRows = 16, kUnitGroups = 8;           // a stage: 16 weight rows by 256 k
-constexpr int kRowPitch = 16 * kUnitGroups + 16;         // 9 chunks: a read of 8 rows covers all banks once
-constexpr int kStageBytes = kUnitRows * kRowPitch + kUnitRows * 2 * kUnitGroups;
+constexpr int kCodeBytes = kUnitRows * 16 * kUnitGroups;  // of a stage; its scales follow all stages' codes
+constexpr int kScaleBytes = kUnitRows * 2 * kUnitGroups;
+constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 
 // W warps, NT blocks of 8 tokens.  SB: bytes a scale copy may take (16, 4 or 2, by the scales' alignment).
 // A block owns a run of weight rows (multiples of 8) in passes of up to W tiles of 16; a pass's tiles
 // times its stages form a line that the warps share evenly, so a tile is cut over two warps at most
 // times (its K is long) and their sums are joined in shared memory, in order.
 template <int W, int NT, int SB>
-__global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
+__global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map, const Args a, int S) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
-  uint2* xf = reinterpret_cast<uint2*>(smem);                                  // [NT][8 KT][32] operands
-  uint8_t* rings = smem + static_cast<size_t>(NT) * KT * kUnitGroups * 256;
+  uint8_t* rings = smem + (-smem_u32(smem) & 1023u);    // [W][S] codes (the swizzle goes by 1024 bytes), then scales
+  uint2* xf = reinterpret_cast<uint2*>(rings + W * S * kStageBytes);            // [NT][8 KT][32] operands
   // sums of the parts of a pass's tiles: the part that warp w has of a tile lies at w + tile, so a tile's
   // parts follow one another in the order of their stages
-  float* red = reinterpret_cast<float*>(rings + W * S * kStageBytes);          // [2 W][8 NT][16]
+  float* red = reinterpret_cast<float*>(xf + static_cast<size_t>(NT) * KT * kUnitGroups * 32);   // [2 W][8 NT][16]
   __shared__ int s_first[W], s_last[W];                                        // a tile's first and last warp
-  const uint32_t ring = smem_u32(rings) + warp * S * kStageBytes;
+  __shared__ uint64_t s_bar[W][6];
+  const uint32_t ring = smem_u32(rings) + warp * S * kCodeBytes;               // codes: 128-byte swizzled rows
+  const uint32_t sring = smem_u32(rings) + W * S * kCodeBytes + warp * S * kScaleBytes;
+  uint64_t* bar = s_bar[warp];
+  if (lane < 6) mbar_init(bar + lane, 1);
+  fence_barrier_init();
+  __syncwarp();
 
   const int64_t R8 = (a.N + 7) / 8;
   const int64_t row_begin = R8 * blockIdx.x / gridDim.x * 8;
@@ -118,38 +128,37 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
     }
     return false;
   };
-  const uint32_t* lane_codes = a.codes + (row_begin + (lane >> 3)) * (a.K >> 3) + (lane & 7) * 4;
+  // Codes come as boxes of 8 rows by 128 bytes, zero past the matrix; a box past this block's rows is left
+  // out (what the stage holds there feeds sums that are not written).
   auto fetch = [&](const Place& p, int st) {
-    const int kt = p.kt, tile16 = (p.pass * W + p.tile) * kUnitRows;
-    const int64_t row0 = row_begin + tile16;
-    const uint32_t base = ring + st * kStageBytes;
-    const int rows = static_cast<int>(min(row_end - row0, static_cast<int64_t>(kUnitRows))) - (lane >> 3);
-    const uint32_t* src = lane_codes + static_cast<int64_t>(tile16) * (a.K >> 3) + kt * (4 * kUnitGroups);
-    const uint32_t dst = base + (lane >> 3) * kRowPitch + (lane & 7) * 16;
-    const bool in_k = kt * kUnitGroups + (lane & 7) < a.KG;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool on = in_k && 4 * i < rows;
-      copy_async<16>(dst + 4 * i * kRowPitch, on ? src + static_cast<int64_t>(4 * i) * (a.K >> 3) : a.codes, on);
-    }
-    const uint32_t sb = base + kUnitRows * kRowPitch;
-    if constexpr (SB == 16) {
-      if (lane < 16) {
-        const bool on = row0 + lane < row_end;
-        copy_async<16>(sb + lane * 16, a.scales + (on ? (row0 + lane) * a.KG + kt * kUnitGroups : 0), on);
+    const int64_t row0 = row_begin + (p.pass * W + p.tile) * kUnitRows;
+    const int rows = static_cast<int>(min(row_end - row0, static_cast<int64_t>(kUnitRows)));
+    if (lane == 0) {
+      const bool both = rows > 8;
+      mbar_arrive_expect_tx(bar + st, (both ? 2 : 1) * (kCodeBytes / 2 + (SB == 16 ? kScaleBytes / 2 : 0)));
+      uint8_t* dst = rings + (warp * S + st) * kCodeBytes;
+      uint8_t* sdst = rings + W * S * kCodeBytes + (warp * S + st) * kScaleBytes;
+      const int y = static_cast<int>(row0);
+      tma_load_2d(dst, &codes_map, p.kt * 4 * kUnitGroups, y, bar + st);
+      if (both) tma_load_2d(dst + kCodeBytes / 2, &codes_map, p.kt * 4 * kUnitGroups, y + 8, bar + st);
+      if constexpr (SB == 16) {
+        tma_load_2d(sdst, &scales_map, p.kt * kUnitGroups, y, bar + st);
+        if (both) tma_load_2d(sdst + kScaleBytes / 2, &scales_map, p.kt * kUnitGroups, y + 8, bar + st);
       }
-    } else if constexpr (SB == 4) {
+    }
+    const uint32_t sb = sring + st * kScaleBytes;
+    if constexpr (SB == 4) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = 8 * i + (lane >> 2), g = kt * kUnitGroups + 2 * (lane & 3);
-        const bool on = row0 + row < row_end && g < a.KG;
+        const int row = 8 * i + (lane >> 2), g = p.kt * kUnitGroups + 2 * (lane & 3);
+        const bool on = row < rows && g < a.KG;
         copy_async<4>(sb + row * 16 + (lane & 3) * 4, a.scales + (on ? (row0 + row) * a.KG + g : 0), on);
       }
-    } else {
+    } else if constexpr (SB == 2) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + (lane >> 3), g = kt * kUnitGroups + (lane & 7);
-        const bool on = row0 + row < row_end && g < a.KG;
+        const int row = 4 * i + (lane >> 3), g = p.kt * kUnitGroups + (lane & 7);
+        const bool on = row < rows && g < a.KG;
         const uint16_t v = on ? ldg_u16(a.scales + (row0 + row) * a.KG + g) : 0;
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(sb + row * 16 + (lane & 7) * 2), "h"(v) : "memory");
       }
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
       fetch(ahead, filled);
       more = advance(ahead);
     }
-    copy_commit();
+    if constexpr (SB == 4) copy_commit();
   }
 
   // the rows as operands, while the first stages are on their way: lane (r, t) of token block b, group g
@@ -211,29 +220,36 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
 #pragma unroll
   for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = 0;
   int st = 0, into = S - 1;
+  uint32_t parity = 0;                                 // of the ring's current round
+  bool alive = true;                                   // false once a bounded wait ran out: no more waits
+  int swz[kUnitGroups];                                // where this lane's word of group g lies in a swizzled row
+#pragma unroll
+  for (int g = 0; g < kUnitGroups; ++g) swz[g] = r * 128 + ((g ^ r) << 4) + t * 4;
   const uint32_t xbase = smem_u32(xf) + lane * 8;
   for (int pass = 0; pass * W < tiles; ++pass) {
     if (have && at.pass == pass) {
       bool first = at.kt == 0;
       while (true) {
-        // S is a run-time number: leave S - 2 groups in flight
-        if (S == 3) copy_wait<1>();
-        else if (S == 4) copy_wait<2>();
-        else if (S == 5) copy_wait<3>();
-        else copy_wait<4>();
+        if (alive) alive = mbar_wait_ring(bar + st, parity);
+        if constexpr (SB == 4) {                         // (S is a run-time number: S - 2 groups stay in flight)
+          if (S == 3) copy_wait<1>();
+          else if (S == 4) copy_wait<2>();
+          else if (S == 5) copy_wait<3>();
+          else copy_wait<4>();
+        }
         __syncwarp();
         if (more) {
           fetch(ahead, into);
           more = advance(ahead);
         }
-        copy_commit();
-        const uint32_t base = ring + st * kStageBytes;
+        if constexpr (SB == 4) copy_commit();
+        const uint32_t base = ring + st * kCodeBytes, sbase = sring + st * kScaleBytes;
         const int kt = at.kt;
-        const uint4 s0 = lds128(base + kUnitRows * kRowPitch + r * 16), s1 = lds128(base + kUnitRows * kRowPitch + (r + 8) * 16);
+        const uint4 s0 = lds128(sbase + r * 16), s1 = lds128(sbase + (r + 8) * 16);
         const uint32_t sw[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
 #pragma unroll
         for (int g = 0; g < kUnitGroups; ++g) {
-          const uint32_t w0 = lds32(base + r * kRowPitch + g * 16 + t * 4), w1 = lds32(base + (r + 8) * kRowPitch + g * 16 + t * 4);
+          const uint32_t w0 = lds32(base + swz[g]), w1 = lds32(base + swz[g] + kCodeBytes / 2);
           const uint32_t a0 = codes_hi(w0 << 4), a1 = codes_hi(w1 << 4), a2 = codes_hi(w0), a3 = codes_hi(w1);
           const uint64_t q0 = twice(g & 1 ? bf16_hi_to_f32(sw[0][g / 2]) : bf16_lo_to_f32(sw[0][g / 2]));
           const uint64_t q1 = twice(g & 1 ? bf16_hi_to_f32(sw[1][g / 2]) : bf16_lo_to_f32(sw[1][g / 2]));
@@ -247,7 +263,10 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
           }
         }
         into = st;
-        st = st + 1 == S ? 0 : st + 1;
+        if (++st == S) {
+          st = 0;
+          parity ^= 1;
+        }
         const int tile = at.tile;
         const bool last = kt == KT - 1;
         have = advance(at);
@@ -298,7 +317,9 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const Args a, int S) {
     }
     __syncthreads();
   }
-  copy_wait<0>();
+  if constexpr (SB == 4) copy_wait<0>();
+  if (!alive)                                          // copies may still be on their way into this block's memory
+    for (int i = 0; i < S; ++i) mbar_wait_ring(bar + i, parity);
 }
 
 // ----------------------------------------------------------------------------------- more rows
@@ -450,7 +471,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const Args a, int splits) {
 }
 
 // ----------------------------------------------------------------------------------- dispatch
-constexpr int kSmemMost = 232448;
+constexpr int kSmemMost = 232448 - 1024 - 1024;   // less the static arrays and the ring's alignment
 
 // How the few-rows kernel is run: W warps, NT token blocks, S stages; S = 0 where the rows leave no room.
 // 16 warps hide the latency of a warp's chain of products better (M 16, N 14336, K 4096: FIG16 us against
@@ -488,12 +509,44 @@ cudaError_t raise_smem(F* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// [rows, wide] elements of `size` bytes as boxes of `box` elements by 8 rows
+bool encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, int64_t rows, int64_t wide, int box,
+            CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(wide), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(wide) * size};
+  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), 8}, estr[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int W, int NT>
 w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t s) {
   auto kernel = SB == 16 ? few_kernel<W, NT, 16> : SB >= 4 ? few_kernel<W, NT, 4> : few_kernel<W, NT, 2>;
-  if (raise_smem(kernel, f.smem) != cudaSuccess) return W4_ERR_CUDA;
+  if (raise_smem(kernel, f.smem + 1024) != cudaSuccess) return W4_ERR_CUDA;
+  CUtensorMap codes, scales;
+  if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kUnitGroups,
+              CU_TENSOR_MAP_SWIZZLE_128B))
+    return W4_ERR_CUDA;
+  if (SB != 16) scales = codes;                        // (not used)
+  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kUnitGroups,
+                   CU_TENSOR_MAP_SWIZZLE_NONE))
+    return W4_ERR_CUDA;
   const int64_t R8 = (a.N + 7) / 8;
-  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * W, f.smem, s>>>(a, f.S);
+  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * W, f.smem + 1024, s>>>(codes, scales, a, f.S);
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

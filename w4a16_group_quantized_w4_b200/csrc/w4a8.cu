@@ -323,25 +323,31 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
 }
 
 // ----------------------------------------------------------------------------------- more rows
-constexpr int kBN = 128, kGS = 4;                        // weight rows of a tile, groups a stage (128 k)
-constexpr int kWPitch = 16 * kGS + 16, kXPitch = 32 * kGS + 32;
-constexpr int kManyStages = 4;
+// Tiles of 128 weight rows by BM tokens, 256 k a stage, everything by TMA into 128-byte swizzled rows.
+// A warp holds MT x NT products (32 weight rows by 32 tokens at BM = 64); the blocks of 8 tokens are read
+// in the order 0, 2, 4, 6, 1, 3, 5, 7, which keeps the 8-byte reads of half a warp free of bank conflicts
+// under the swizzle.  Bound by instructions: about ten a product, of which four are the float32 pairs.
+constexpr int kBN = 128, kGS = 8;                        // weight rows of a tile, groups a stage
 
 template <int BM>
 struct Many {
   static constexpr int WR = BM >= 64 ? 4 : 8, WC = 8 / WR;         // warps over rows, over tokens
   static constexpr int MT = kBN / 16 / WR, NT = BM / 8 / WC;       // 16-row and 8-token blocks of a warp
-  static constexpr int kScales = kBN * kWPitch, kX = kScales + kBN * 2 * kGS;
-  static constexpr int kStage = kX + BM * kXPitch;
+  static constexpr int S = 3;
+  static constexpr int kX = kBN * 16 * kGS, kScales = kX + 2 * BM * 128, kStage = kScales + kBN * 2 * kGS;
   static constexpr int kOut = BM * (kBN + 4) * 4;
-  static constexpr int kSmem = kManyStages * kStage > kOut ? kManyStages * kStage : kOut;
+  static constexpr int kSmem = (S * kStage > kOut ? S * kStage : kOut) + 1024;
 };
 
 // blockIdx.x: token tile (fastest, so that a weight tile is shared in L2), y: row tile, z: part of K.
 template <int BM, int SB>
-__global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
+__global__ void __launch_bounds__(256, 2)
+many_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map,
+            const __grid_constant__ CUtensorMap x_map, const Args a) {
   using C = Many<BM>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem_[];
+  uint8_t* smem = smem_ + (-smem_u32(smem_) & 1023u);
+  __shared__ uint64_t s_bar[C::S];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int wr = warp % C::WR, wc = warp / C::WR;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * BM, n0 = static_cast<int64_t>(blockIdx.y) * kBN;
@@ -349,37 +355,28 @@ __global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
   const int k0 = static_cast<int>(static_cast<int64_t>(KT) * blockIdx.z / gridDim.z);
   const int k1 = static_cast<int>(static_cast<int64_t>(KT) * (blockIdx.z + 1) / gridDim.z);
   const uint32_t s0 = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::S; ++i) mbar_init(s_bar + i, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
 
   auto fetch = [&](int kt, int st) {
-    const uint32_t base = s0 + st * C::kStage;
-#pragma unroll
-    for (int i = 0; i < kBN * kGS / 256; ++i) {
-      const int c = i * 256 + threadIdx.x, row = c / kGS, g = kt * kGS + c % kGS;
-      const bool on = n0 + row < a.N && g < a.KG;
-      copy_async<16>(base + row * kWPitch + (c % kGS) * 16, a.codes + (on ? (n0 + row) * (a.K >> 3) + g * 4 : 0), on);
+    uint8_t* base = smem + st * C::kStage;
+    if (threadIdx.x == 0) {
+      mbar_arrive_expect_tx(s_bar + st, SB == 16 ? C::kStage : C::kScales);
+      tma_load_2d(base, &codes_map, kt * 4 * kGS, static_cast<int>(n0), s_bar + st);
+      tma_load_2d(base + C::kX, &x_map, kt * 256, static_cast<int>(m0), s_bar + st);
+      tma_load_2d(base + C::kX + BM * 128, &x_map, kt * 256 + 128, static_cast<int>(m0), s_bar + st);
+      if constexpr (SB == 16) tma_load_2d(base + C::kScales, &scales_map, kt * kGS, static_cast<int>(n0), s_bar + st);
     }
-    if constexpr (SB >= 8) {
-      if (threadIdx.x < kBN) {
-        const int row = threadIdx.x;
-        const bool on = n0 + row < a.N;
-        copy_async<8>(base + C::kScales + row * 8, a.scales + (on ? (n0 + row) * a.KG + kt * kGS : 0), on);
-      }
-    } else if constexpr (SB == 4) {
-      const int row = threadIdx.x >> 1, g = kt * kGS + 2 * (threadIdx.x & 1);
-      const bool on = n0 + row < a.N && g < a.KG;
-      copy_async<4>(base + C::kScales + threadIdx.x * 4, a.scales + (on ? (n0 + row) * a.KG + g : 0), on);
-    } else {
+    if constexpr (SB != 16) {                            // (visible with the block's next barrier)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kBN * kGS / 256; ++i) {
         const int c = i * 256 + threadIdx.x, row = c / kGS, g = kt * kGS + c % kGS;
         const uint16_t v = n0 + row < a.N && g < a.KG ? ldg_u16(a.scales + (n0 + row) * a.KG + g) : 0;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + C::kScales + c * 2), "h"(v) : "memory");
+        *reinterpret_cast<uint16_t*>(base + C::kScales + c * 2) = v;
       }
-    }
-    for (int c = threadIdx.x; c < BM * 2 * kGS; c += 256) {
-      const int row = c / (2 * kGS), col = c % (2 * kGS), k = kt * kGS * 32 + col * 16;
-      const bool on = m0 + row < a.M && k < a.K;
-      copy_async<16>(base + C::kX + row * kXPitch + col * 16, a.x + (on ? (m0 + row) * a.K + k : 0), on);
     }
   };
 
@@ -389,38 +386,40 @@ __global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < C::NT; ++j) acc[i][j][0] = acc[i][j][1] = 0;
 
-  for (int i = 0; i < kManyStages - 1; ++i) {
+  for (int i = 0; i < C::S - 1; ++i)
     if (k0 + i < k1) fetch(k0 + i, i);
-    copy_commit();
-  }
+  const int tok = 2 * (r & 3) + (r >> 2);                  // the token of this lane's operand, of 8
+  const uint32_t wb = s0 + (wr * C::MT * 16 + r) * 128 + t * 4;
+  const uint32_t xb = s0 + C::kX + (wc * C::NT * 8 + tok) * 128 + (t & 1) * 8;
   int st = 0;
+  uint32_t parity = 0;
+  bool alive = true;                                       // false once a bounded wait ran out: no more waits
   for (int kt = k0; kt < k1; ++kt) {
-    copy_wait<kManyStages - 2>();
+    if (alive) alive = mbar_wait_ring(s_bar + st, parity);
     __syncthreads();
-    if (kt + kManyStages - 1 < k1) fetch(kt + kManyStages - 1, (st + kManyStages - 1) % kManyStages);
-    copy_commit();
-    const uint32_t base = s0 + st * C::kStage;
-    const uint32_t wb = base + (wr * C::MT * 16 + r) * kWPitch + t * 4;
-    const uint32_t xb = base + C::kX + (wc * C::NT * 8 + r) * kXPitch + t * 8;
-    uint2 sw[C::MT][2];
+    if (kt + C::S - 1 < k1) fetch(kt + C::S - 1, st == 0 ? C::S - 1 : st - 1);
+    const uint32_t off = st * C::kStage;
+    uint4 sw[C::MT][2];
 #pragma unroll
     for (int i = 0; i < C::MT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) sw[i][h] = lds64(base + C::kScales + (wr * C::MT * 16 + i * 16 + h * 8 + r) * 8);
+      for (int h = 0; h < 2; ++h) sw[i][h] = lds128(s0 + off + C::kScales + (wr * C::MT * 16 + i * 16 + h * 8 + r) * 16);
 #pragma unroll
     for (int g = 0; g < kGS; ++g) {
       uint32_t xe[C::NT], xo[C::NT];
+      const uint32_t xg = xb + off + (g / 4) * (BM * 128) + (((2 * (g % 4) + (t >> 1)) ^ tok) << 4);
+      const uint32_t wg = wb + off + ((g ^ r) << 4);
 #pragma unroll
       for (int j = 0; j < C::NT; ++j) {
-        const uint2 x = lds64(xb + j * 8 * kXPitch + g * 32);
+        const uint2 x = lds64(xg + j * 1024);
         xe[j] = __byte_perm(x.x, x.y, 0x6420);
         xo[j] = __byte_perm(x.x, x.y, 0x7531);
       }
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) {
-        const uint32_t w0 = lds32(wb + i * 16 * kWPitch + g * 16), w1 = lds32(wb + (i * 16 + 8) * kWPitch + g * 16);
+        const uint32_t w0 = lds32(wg + i * 2048), w1 = lds32(wg + i * 2048 + 1024);
         const uint32_t a0 = codes_hi(w0 << 4), a1 = codes_hi(w1 << 4), a2 = codes_hi(w0), a3 = codes_hi(w1);
-        const uint32_t p0 = g < 2 ? sw[i][0].x : sw[i][0].y, p1 = g < 2 ? sw[i][1].x : sw[i][1].y;
+        const uint32_t p0 = reinterpret_cast<const uint32_t*>(&sw[i][0])[g / 2], p1 = reinterpret_cast<const uint32_t*>(&sw[i][1])[g / 2];
         const uint64_t q0 = twice(g & 1 ? bf16_hi_to_f32(p0) : bf16_lo_to_f32(p0));
         const uint64_t q1 = twice(g & 1 ? bf16_hi_to_f32(p1) : bf16_lo_to_f32(p1));
 #pragma unroll
@@ -432,9 +431,13 @@ __global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
         }
       }
     }
-    st = st + 1 == kManyStages ? 0 : st + 1;
+    if (++st == C::S) {
+      st = 0;
+      parity ^= 1;
+    }
   }
-  copy_wait<0>();
+  if (!alive)                                              // copies may still be on their way into this block's memory
+    for (int i = 0; i < C::S; ++i) mbar_wait_ring(s_bar + i, parity);
   __syncthreads();
   float* o = reinterpret_cast<float*>(smem);               // [token][kBN + 4]
 #pragma unroll
@@ -445,9 +448,10 @@ __global__ void __launch_bounds__(256, 2) many_kernel(const Args a) {
       for (int h = 0; h < 2; ++h) {
         float lo, hi;
         halves(acc[i][j][h], lo, hi);
-        const int m = wc * C::NT * 8 + j * 8 + 2 * t, n = wr * C::MT * 16 + i * 16 + h * 8 + r;
-        o[m * (kBN + 4) + n] = lo;
-        o[(m + 1) * (kBN + 4) + n] = hi;
+        // columns 2 t and 2 t + 1 of the product are these tokens
+        const int m = wc * C::NT * 8 + j * 8, n = wr * C::MT * 16 + i * 16 + h * 8 + r;
+        o[(m + 4 * (t & 1) + (t >> 1)) * (kBN + 4) + n] = lo;
+        o[(m + 4 * (t & 1) + 2 + (t >> 1)) * (kBN + 4) + n] = hi;
       }
   __syncthreads();
   for (int i = threadIdx.x; i < BM * kBN; i += 256) {
@@ -474,8 +478,8 @@ __global__ void __launch_bounds__(256) parts_kernel(const Args a, int splits) {
 constexpr int kSmemMost = 232448 - 1024 - 1024;   // less the static arrays and the ring's alignment
 
 // How the few-rows kernel is run: W warps, NT token blocks, S stages; S = 0 where the rows leave no room.
-// 16 warps hide the latency of a warp's chain of products better (M 16, N 14336, K 4096: FIG16 us against
-// FIG8 us with 8), where their rings fit.
+// 16 warps hide the latency of a warp's chain of products better (M 16, N 14336, K 4096: 17.9 us against
+// 19.8 us with 8 when it was chosen), where their rings fit.
 struct Few {
   int W, NT, S, smem;
 };
@@ -495,11 +499,11 @@ Few few_plan(int64_t M, int64_t KG) {
 
 int many_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-// Parts of K: enough to give every SM a block, each at least 1024 k long
+// Parts of K: enough to give every SM two blocks, each at least 1024 k long
 int many_splits(int64_t M, int64_t N, int64_t KG, int sms) {
   const int BM = many_tile(M);
   const int64_t tiles = (M + BM - 1) / BM * ((N + kBN - 1) / kBN);
-  const int64_t want = sms / tiles, most = KG / 32;
+  const int64_t want = 2 * sms / tiles, most = KG / 32;
   const int64_t s = want < most ? want : most;
   return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
 }
@@ -521,14 +525,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [rows, wide] elements of `size` bytes as boxes of `box` elements by 8 rows
+// [rows, wide] elements of `size` bytes as boxes of `box` elements by `high` rows
 bool encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, int64_t rows, int64_t wide, int box,
-            CUtensorMapSwizzle swizzle) {
+            int high, CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(wide), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(wide) * size};
-  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), 8}, estr[2] = {1, 1};
+  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(high)}, estr[2] = {1, 1};
   return fn(m, type, 2, const_cast<void*>(p), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -538,11 +542,11 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
   auto kernel = SB == 16 ? few_kernel<W, NT, 16> : SB >= 4 ? few_kernel<W, NT, 4> : few_kernel<W, NT, 2>;
   if (raise_smem(kernel, f.smem + 1024) != cudaSuccess) return W4_ERR_CUDA;
   CUtensorMap codes, scales;
-  if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kUnitGroups,
+  if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kUnitGroups, 8,
               CU_TENSOR_MAP_SWIZZLE_128B))
     return W4_ERR_CUDA;
   if (SB != 16) scales = codes;                        // (not used)
-  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kUnitGroups,
+  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kUnitGroups, 8,
                    CU_TENSOR_MAP_SWIZZLE_NONE))
     return W4_ERR_CUDA;
   const int64_t R8 = (a.N + 7) / 8;
@@ -558,12 +562,19 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
 
 template <int BM>
 w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s) {
-  auto kernel = SB >= 8 ? many_kernel<BM, 8> : SB == 4 ? many_kernel<BM, 4> : many_kernel<BM, 2>;
+  auto kernel = SB == 16 ? many_kernel<BM, 16> : many_kernel<BM, 2>;
   if (raise_smem(kernel, Many<BM>::kSmem) != cudaSuccess) return W4_ERR_CUDA;
+  CUtensorMap codes, scales, x;
+  if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kGS, kBN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.M, a.K, 128, BM, CU_TENSOR_MAP_SWIZZLE_128B))
+    return W4_ERR_CUDA;
+  if (SB != 16) scales = codes;                        // (not used)
+  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kGS, kBN, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return W4_ERR_CUDA;
   const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + kBN - 1) / kBN;
   if (tm > 0x7FFFFFFFLL || tn > 65535) return W4_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(tm), static_cast<unsigned>(tn), splits);
-  kernel<<<grid, 256, Many<BM>::kSmem, s>>>(a);
+  kernel<<<grid, 256, Many<BM>::kSmem, s>>>(codes, scales, x, a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
   if (splits == 1) return W4_OK;
   const int64_t blocks = (a.M * a.N + 255) / 256;
@@ -591,7 +602,7 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   if (M > 0 && (!xq || !xs || !y)) return W4_ERR_INVALID_ARG;
   if (!aligned_to(xq, 16) || !aligned_to(xs, 4) || !aligned_to(y, 16) || !aligned_to(workspace, 16))
     return W4_ERR_INVALID_ARG;
-  if (M > (1LL << 40) / N) return W4_ERR_UNSUPPORTED;
+  if (M > (1LL << 40) / N || M > 0x7FFFFFFFLL) return W4_ERR_UNSUPPORTED;
   if (M == 0) return W4_OK;
   const size_t need = w4_linear8_workspace_bytes(M, N, K);
   if (need && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;

@@ -402,7 +402,20 @@ def _device_call(fn):
 
 
 def _cur(dev) -> int:
+    """The raw handle of dev's current stream (without building a Stream object, where torch allows)."""
+    if _RAW_STREAM is not None:
+        return _RAW_STREAM(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fits(name, t, dtype, shape, dev):
+    """_need's checks in one cheap expression; the details only when it fails."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(name, t, dtype, shape, dev)
 
 
 def _ptr(t):
@@ -411,39 +424,56 @@ def _ptr(t):
 
 def _rows3(name, t, heads, dim, dev):
     """A bf16 [T, heads, dim] tensor whose rows may be columns of a wider one; its row stride."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name}: expected device {dev}, got {t.device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: expected shape [rows, {heads}, {dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: expected shape [rows, {heads}, {dim}], got {tuple(shape)}")
     s = t.stride()
-    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
         raise ValueError(f"{name}: heads and elements of a row must be contiguous")
-    return s[0] if t.shape[0] > 1 else heads * dim
+    return s[0] if shape[0] > 1 else heads * dim
 
 
-def _scratch(nbytes: int, dev):
-    """Scratch for one call, from torch's stream-ordered allocator: calls on different streams never
-    share it, and a call captured into a CUDA graph keeps it in that graph's own pool."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+@functools.lru_cache(maxsize=4096)
+def _bytes_needed(op, m, n, k, e, index):
+    """w4_workspace_bytes on the current device (whose index only keys the cache)."""
+    return int(_lib.load().w4_workspace_bytes(op, m, n, k, e, 0))
+
+
+def _scratch(ws, nbytes: int, dev):
+    """(pointer, size, tensor to keep) of a call's scratch: ws, or one from torch's stream-ordered
+    allocator, so that calls on different streams never share it and a call captured into a CUDA
+    graph keeps it in that graph's own pool."""
+    if ws is None:
+        if not nbytes:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), nbytes, ws
+    _need("ws", ws, torch.uint8, None, dev)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def _rms_args(x, residual, weight, h):
-    if x.dim() != 2:
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _need("x", x, torch.bfloat16)
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x: expected two dimensions")
-    T, H = x.shape
     dev = x.device
-    _need("x", x, torch.bfloat16)
     if residual is not None:
-        _need("residual", residual, torch.bfloat16, (T, H), dev)
-        h = torch.empty_like(x) if h is None else h
-        _need("h", h, torch.bfloat16, (T, H), dev)
+        _fits("residual", residual, torch.bfloat16, shape, dev)
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _fits("h", h, torch.bfloat16, shape, dev)
     elif h is not None:
         raise ValueError("h: only written when a residual is given")
     if weight is not None:
-        _need("weight", weight, torch.bfloat16, (H,), dev)
-    return T, H, dev, h
+        _fits("weight", weight, torch.bfloat16, shape[1:], dev)
+    return shape, dev, h
 
 
 @_device_call
@@ -451,49 +481,58 @@ def w4_rms_add(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, y=No
     """h = bf16(x + residual), y = bf16(h * weight / sqrt(mean over each row of h^2 + eps)); bf16
     [T, H] -> (y, h).  h is x itself without a residual; h may be passed as the residual's own
     buffer to update it in place."""
-    T, H, dev, h = _rms_args(x, residual, weight, h)
-    y = torch.empty_like(x) if y is None else y
-    _need("y", y, torch.bfloat16, (T, H), dev)
-    _lib.check("w4_rms_add", _lib.load().w4_rms_add(
-        x.data_ptr(), _ptr(residual), _ptr(weight), T, H, eps, _ptr(h), y.data_ptr(), _cur(dev)))
+    shape, dev, h = _rms_args(x, residual, weight, h)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _fits("y", y, torch.bfloat16, shape, dev)
+    st = _lib.load().w4_rms_add(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h),
+                                y.data_ptr(), _cur(dev))
+    if st:
+        _lib.check("w4_rms_add", st)
     return y, x if h is None else h
 
 
 @_device_call
 def w4_rms_add_q8(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, q=None, q_scale=None):
     """w4_rms_add with 8-bit rows: (q int8 [T, H], q_scale f32 [T], h), y = q_scale * q."""
-    T, H, dev, h = _rms_args(x, residual, weight, h)
-    q = torch.empty((T, H), dtype=torch.int8, device=dev) if q is None else q
-    q_scale = torch.empty(T, dtype=torch.float32, device=dev) if q_scale is None else q_scale
-    _need("q", q, torch.int8, (T, H), dev)
-    _need("q_scale", q_scale, torch.float32, (T,), dev)
-    _lib.check("w4_rms_add_q8", _lib.load().w4_rms_add_q8(
-        x.data_ptr(), _ptr(residual), _ptr(weight), T, H, eps, _ptr(h), q.data_ptr(), q_scale.data_ptr(), _cur(dev)))
+    shape, dev, h = _rms_args(x, residual, weight, h)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=dev)
+    else:
+        _fits("q", q, torch.int8, shape, dev)
+    if q_scale is None:
+        q_scale = torch.empty(shape[0], dtype=torch.float32, device=dev)
+    else:
+        _fits("q_scale", q_scale, torch.float32, shape[:1], dev)
+    st = _lib.load().w4_rms_add_q8(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h),
+                                   q.data_ptr(), q_scale.data_ptr(), _cur(dev))
+    if st:
+        _lib.check("w4_rms_add_q8", st)
     return q, q_scale, x if h is None else h
 
 
 @_device_call
 def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
     """y [M, N] = xs * (xq [M, K] int8 @ dequant(codes, scales)^T), bf16 out."""
-    lib = _lib.load()
     if xq.dim() != 2 or codes.dim() != 2:
         raise ValueError("xq, codes: expected two dimensions")
     M, K = xq.shape
     N = codes.shape[0]
     dev = xq.device
-    _need("xq", xq, torch.int8)
-    _need("xs", xs, torch.float32, (M,), dev)
-    _need("codes", codes, torch.int32, (N, K // 8), dev)
-    _need("scales", scales, torch.bfloat16, (N, K // 32), dev)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
-    _need("y", y, torch.bfloat16, (M, N), dev)
-    if ws is None:
-        ws = _scratch(lib.w4_workspace_bytes(_lib.W4_OP_LINEAR_8, M, N, K, 1, 1), dev)
+    _fits("xq", xq, torch.int8, (M, K), dev)
+    _fits("xs", xs, torch.float32, (M,), dev)
+    _fits("codes", codes, torch.int32, (N, K // 8), dev)
+    _fits("scales", scales, torch.bfloat16, (N, K // 32), dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     else:
-        _need("ws", ws, torch.uint8, None, dev)
-    _lib.check("w4a8_linear", lib.w4a8_linear(
-        xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K,
-        _ptr(ws), 0 if ws is None else ws.numel(), _cur(dev)))
+        _fits("y", y, torch.bfloat16, (M, N), dev)
+    p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_LINEAR_8, M, N, K, 1, dev.index), dev)
+    st = _lib.load().w4a8_linear(xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M,
+                                 N, K, p, n, _cur(dev))
+    if st:
+        _lib.check("w4a8_linear", st)
     return y
 
 
@@ -502,22 +541,25 @@ _KV_KINDS = {torch.bfloat16: (_lib.W4_KV_BF16, 1), torch.int8: (_lib.W4_KV_INT8,
 
 def _cache_args(k_cache, v_cache, k_scales, v_scales, dev):
     """(kind, kv_heads, head_dim, pages, page_size) of a cache, its tensors checked."""
-    if k_cache.dtype not in _KV_KINDS:
-        raise TypeError(f"k_cache: expected bfloat16, int8 or int32 words, got {k_cache.dtype}")
-    kind, per = _KV_KINDS[k_cache.dtype]
-    if k_cache.dim() != 4:
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache: expected a torch.Tensor")
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if dtype not in _KV_KINDS:
+        raise TypeError(f"k_cache: expected bfloat16, int8 or int32 words, got {dtype}")
+    kind, per = _KV_KINDS[dtype]
+    if len(shape) != 4:
         raise ValueError("k_cache: expected [pages, kv_heads, page_size, head_dim]")
-    _need("k_cache", k_cache, k_cache.dtype, None, dev)
-    _need("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
-    pages, heads, page_size, dim = k_cache.shape
+    _fits("k_cache", k_cache, dtype, shape, dev)
+    _fits("v_cache", v_cache, dtype, shape, dev)
+    pages, heads, page_size, dim = shape
     dim *= per
     if kind == _lib.W4_KV_BF16:
         if k_scales is not None or v_scales is not None:
             raise ValueError("k_scales, v_scales: a bfloat16 cache has none")
     else:
         want = (pages, heads, page_size, dim // 32)
-        _need("k_scales", k_scales, torch.bfloat16, want, dev)
-        _need("v_scales", v_scales, torch.bfloat16, want, dev)
+        _fits("k_scales", k_scales, torch.bfloat16, want, dev)
+        _fits("v_scales", v_scales, torch.bfloat16, want, dev)
     return kind, heads, dim, pages, page_size
 
 
@@ -528,16 +570,18 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None, 
     or int4 (int32 words)."""
     dev = k.device
     kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
-    T = k.shape[0]
     ks, vs = _rows3("k", k, heads, dim, dev), _rows3("v", v, heads, dim, dev)
+    T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"v: expected {T} rows, got {v.shape[0]}")
-    _need("slots", slots, torch.int64, (T,), dev)
+    _fits("slots", slots, torch.int64, (T,), dev)
     if dev_status is not None:
-        _need("dev_status", dev_status, torch.int32, (1,), dev)
-    _lib.check("kv_cache_write", _lib.load().kv_cache_write(
+        _fits("dev_status", dev_status, torch.int32, (1,), dev)
+    st = _lib.load().kv_cache_write(
         k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, kind, heads, dim, pages, page_size,
-        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _ptr(dev_status), _cur(dev)))
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _ptr(dev_status), _cur(dev))
+    if st:
+        _lib.check("kv_cache_write", st)
 
 
 @_device_call
@@ -546,16 +590,23 @@ def kv_cache_read(slots, k_cache, v_cache, k_scales=None, v_scales=None, k=None,
     dev = slots.device
     kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
     T = slots.shape[0]
-    _need("slots", slots, torch.int64, (T,), dev)
-    k = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev) if v is None else v
-    _need("k", k, torch.bfloat16, (T, heads, dim), dev)
-    _need("v", v, torch.bfloat16, (T, heads, dim), dev)
+    _fits("slots", slots, torch.int64, (T,), dev)
+    want = (T, heads, dim)
+    if k is None:
+        k = torch.empty(want, dtype=torch.bfloat16, device=dev)
+    else:
+        _fits("k", k, torch.bfloat16, want, dev)
+    if v is None:
+        v = torch.empty(want, dtype=torch.bfloat16, device=dev)
+    else:
+        _fits("v", v, torch.bfloat16, want, dev)
     if dev_status is not None:
-        _need("dev_status", dev_status, torch.int32, (1,), dev)
-    _lib.check("kv_cache_read", _lib.load().kv_cache_read(
+        _fits("dev_status", dev_status, torch.int32, (1,), dev)
+    st = _lib.load().kv_cache_read(
         slots.data_ptr(), T, kind, heads, dim, pages, page_size, k_cache.data_ptr(), v_cache.data_ptr(),
-        _ptr(k_scales), _ptr(v_scales), k.data_ptr(), v.data_ptr(), _ptr(dev_status), _cur(dev)))
+        _ptr(k_scales), _ptr(v_scales), k.data_ptr(), v.data_ptr(), _ptr(dev_status), _cur(dev))
+    if st:
+        _lib.check("kv_cache_read", st)
     return k, v
 
 
@@ -566,33 +617,34 @@ def kv_cache_attend(q, k_cache, v_cache, page_table, seq_lens, k_scales=None, v_
     over the cached tokens named by page_table int32 [B, width] and seq_lens int32 [B] -> out bf16
     [B, q_heads, head_dim].  scale: 1 / sqrt(head_dim) when None; softcap, window: 0 for none;
     lse: float32 [B, q_heads] to receive log sum exp(score)."""
-    lib = _lib.load()
     dev = q.device
     kind, heads, dim, pages, page_size = _cache_args(k_cache, v_cache, k_scales, v_scales, dev)
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q: expected [B, q_heads, head_dim]")
-    B, q_heads, _ = q.shape
+    B, q_heads, _ = shape
     qs = _rows3("q", q, q_heads, dim, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table: expected [B, width]")
     width = page_table.shape[1]
-    _need("page_table", page_table, torch.int32, (B, width), dev)
-    _need("seq_lens", seq_lens, torch.int32, (B,), dev)
-    out = torch.empty((B, q_heads, dim), dtype=torch.bfloat16, device=dev) if out is None else out
-    _need("out", out, torch.bfloat16, (B, q_heads, dim), dev)
-    if lse is not None:
-        _need("lse", lse, torch.float32, (B, q_heads), dev)
-    if dev_status is not None:
-        _need("dev_status", dev_status, torch.int32, (1,), dev)
-    if ws is None:
-        ws = _scratch(lib.w4_workspace_bytes(_lib.W4_OP_ATTEND, B, q_heads, dim, heads, 0), dev)
+    _fits("page_table", page_table, torch.int32, (B, width), dev)
+    _fits("seq_lens", seq_lens, torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _need("ws", ws, torch.uint8, None, dev)
-    _lib.check("kv_cache_attend", lib.kv_cache_attend(
+        _fits("out", out, torch.bfloat16, shape, dev)
+    if lse is not None:
+        _fits("lse", lse, torch.float32, (B, q_heads), dev)
+    if dev_status is not None:
+        _fits("dev_status", dev_status, torch.int32, (1,), dev)
+    p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_ATTEND, B, q_heads, dim, heads, dev.index), dev)
+    st = _lib.load().kv_cache_attend(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind,
         page_table.data_ptr(), width, seq_lens.data_ptr(), B, q_heads, heads, dim, pages, page_size,
-        dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _ptr(lse), _ptr(ws),
-        0 if ws is None else ws.numel(), _ptr(dev_status), _cur(dev)))
+        dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _ptr(lse), p, n, _ptr(dev_status),
+        _cur(dev))
+    if st:
+        _lib.check("kv_cache_attend", st)
     return out
 
 

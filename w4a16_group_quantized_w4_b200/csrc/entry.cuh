@@ -38,4 +38,20 @@ inline int device_sm_count() {
   return n;
 }
 
+// Raises a kernel's limit of dynamic shared memory to `bytes`, once per device and value.
+// `raised` is the kernel's own static table.
+struct SmemRaised {
+  int bytes[64] = {0};
+};
+template <typename F>
+inline cudaError_t raise_smem(F* kernel, int bytes, SmemRaised& raised) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && raised.bytes[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) raised.bytes[dev] = bytes;
+  return e;
+}
+
 }  // namespace w4

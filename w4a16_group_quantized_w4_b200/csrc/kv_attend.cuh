@@ -920,10 +920,11 @@ int grid_of(const Args& a, int sms) {
 template <int KIND, int D>
 w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
   const int grid = grid_of<KIND, D>(a, sms);
-  auto kernel = a.page_size % 16 == 0 ? attend_kernel<KIND, D, true> : attend_kernel<KIND, D, false>;
+  const bool u16 = a.page_size % 16 == 0;
+  auto kernel = u16 ? attend_kernel<KIND, D, true> : attend_kernel<KIND, D, false>;
   constexpr int kSmem = Cfg<KIND, D>::kSmem;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return W4_ERR_CUDA;
+  static SmemRaised raised[2];
+  if (raise_smem(kernel, kSmem, raised[u16]) != cudaSuccess) return W4_ERR_CUDA;
   kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
   if (grid == 1) return W4_OK;                           // nothing is split

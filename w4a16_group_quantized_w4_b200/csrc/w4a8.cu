@@ -75,6 +75,7 @@ struct Args {
   uint16_t* y;
   int64_t M, N;
   int K, KG;                       // KG = K / 32 groups
+  int eights, more;                // few rows: a block's runs of 8 weight rows; the first `more` have one more
   float* parts;                    // [splits][M][N], when K is split over blocks
 };
 
@@ -107,9 +108,9 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
   fence_barrier_init();
   __syncwarp();
 
-  const int64_t R8 = (a.N + 7) / 8;
-  const int64_t row_begin = R8 * blockIdx.x / gridDim.x * 8;
-  const int64_t row_end = min(a.N, R8 * (blockIdx.x + 1) / gridDim.x * 8);
+  const int c = blockIdx.x;
+  const int64_t row_begin = (static_cast<int64_t>(c) * a.eights + min(c, a.more)) * 8;
+  const int64_t row_end = min(a.N, row_begin + (a.eights + (c < a.more ? 1 : 0)) * 8);
   const int tiles = static_cast<int>((row_end - row_begin + kUnitRows - 1) / kUnitRows);
   if (tiles <= 0) return;
 
@@ -508,11 +509,6 @@ int many_splits(int64_t M, int64_t N, int64_t KG, int sms) {
   return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
 }
 
-template <typename F>
-cudaError_t raise_smem(F* kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -540,7 +536,8 @@ bool encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int size, i
 template <int W, int NT>
 w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t s) {
   auto kernel = SB == 16 ? few_kernel<W, NT, 16> : SB >= 4 ? few_kernel<W, NT, 4> : few_kernel<W, NT, 2>;
-  if (raise_smem(kernel, f.smem + 1024) != cudaSuccess) return W4_ERR_CUDA;
+  static SmemRaised raised[3];
+  if (raise_smem(kernel, kSmemMost + 1024, raised[SB == 16 ? 0 : SB >= 4 ? 1 : 2]) != cudaSuccess) return W4_ERR_CUDA;
   CUtensorMap codes, scales;
   if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kUnitGroups, 8,
               CU_TENSOR_MAP_SWIZZLE_128B))
@@ -550,7 +547,11 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
                    CU_TENSOR_MAP_SWIZZLE_NONE))
     return W4_ERR_CUDA;
   const int64_t R8 = (a.N + 7) / 8;
-  kernel<<<static_cast<unsigned>(R8 < sms ? R8 : sms), 32 * W, f.smem + 1024, s>>>(codes, scales, a, f.S);
+  const int grid = static_cast<int>(R8 < sms ? R8 : sms);
+  Args b = a;
+  b.eights = static_cast<int>(R8 / grid);
+  b.more = static_cast<int>(R8 % grid);
+  kernel<<<grid, 32 * W, f.smem + 1024, s>>>(codes, scales, b, f.S);
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
@@ -563,7 +564,8 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
 template <int BM>
 w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s) {
   auto kernel = SB == 16 ? many_kernel<BM, 16> : many_kernel<BM, 2>;
-  if (raise_smem(kernel, Many<BM>::kSmem) != cudaSuccess) return W4_ERR_CUDA;
+  static SmemRaised raised[2];
+  if (raise_smem(kernel, Many<BM>::kSmem, raised[SB == 16]) != cudaSuccess) return W4_ERR_CUDA;
   CUtensorMap codes, scales, x;
   if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kGS, kBN, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&x, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.M, a.K, 128, BM, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -606,7 +608,7 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   if (M == 0) return W4_OK;
   const size_t need = w4_linear8_workspace_bytes(M, N, K);
   if (need && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
-  a8::Args a{xq, xs, codes, scales, y, M, N, static_cast<int>(K), static_cast<int>(K / 32), static_cast<float*>(workspace)};
+  a8::Args a{xq, xs, codes, scales, y, M, N, static_cast<int>(K), static_cast<int>(K / 32), 0, 0, static_cast<float*>(workspace)};
   auto s = static_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
   // what a copy of consecutive scales may take at once: every row starts at a multiple of it

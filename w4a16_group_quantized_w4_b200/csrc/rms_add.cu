@@ -6,7 +6,8 @@
 // h_i * w_i is exact in float32 (two 8-bit significands), and multiplication by one positive
 // number keeps the order, so max|y| = max|h w| * (1 / rms): both row statistics come out of one
 // pass over registers and one reduction, and every input byte is read once.  The 8-bit form takes
-// s = max|y| / 127 and q_i = rint(y_i / s).
+// s = max|y| / 127 and q_i = rint(y_i / s) = rint(h_i w_i * (127 / max|h w|)): one fused multiply and add
+// of 1.5 * 2^23, which leaves the rounded integer in the low bits.
 //
 // Bound by memory: x, residual and h at 2 bytes an element, y at 2 or 1.  A row is held in the
 // registers of 1 to 32 warps, CPT 16-byte chunks a thread; short rows share a block, so that a
@@ -96,6 +97,7 @@ rms_add_kernel(const uint16_t* __restrict__ x, const uint16_t* residual, const u
     s = finite ? __uint_as_float(amax) * inv / 127.f : __int_as_float(0x7FC00000);
     if (tid == 0) q_scale[row] = s;
   }
+  const float up = Q8 ? 127.f / __uint_as_float(amax) : 0.f;
 #pragma unroll
   for (int c = 0; c < CPT; ++c) {
     const int i = c * tpr + tid;
@@ -107,20 +109,29 @@ rms_add_kernel(const uint16_t* __restrict__ x, const uint16_t* residual, const u
     float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_lo_to_f32(hw[j]) * bf16_lo_to_f32(ww[j]) * inv;
-      v[2 * j + 1] = bf16_hi_to_f32(hw[j]) * bf16_hi_to_f32(ww[j]) * inv;
+      v[2 * j] = bf16_lo_to_f32(hw[j]) * bf16_lo_to_f32(ww[j]);
+      v[2 * j + 1] = bf16_hi_to_f32(hw[j]) * bf16_hi_to_f32(ww[j]);
     }
     if (Q8) {
-      uint32_t o[2] = {0, 0};
-      if (finite && s > 0.f) {
+      uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int code = max(-127, min(127, __float2int_rn(__fdiv_rn(v[j], s))));
-          o[j >> 2] |= static_cast<uint32_t>(code & 0xFF) << (8 * (j & 3));
+      for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(fmaf(v[j], up, 12582912.f));
+      uint2 o = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                           __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+      if (!(finite && s >= 0x1p-126f)) {
+        // no scale to speak of, or a subnormal one, which need not be close to max / 127
+        o = make_uint2(0, 0);
+        if (finite && s > 0.f) {
+          uint32_t b[2] = {0, 0};
+          for (int j = 0; j < 8; ++j)
+            b[j >> 2] |= static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(v[j] * inv, s)))) & 0xFF) << (8 * (j & 3));
+          o = make_uint2(b[0], b[1]);
         }
       }
-      reinterpret_cast<uint2*>(q + row * H)[i] = make_uint2(o[0], o[1]);
+      reinterpret_cast<uint2*>(q + row * H)[i] = o;
     } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
       reinterpret_cast<uint4*>(y + row * H)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }

@@ -8,40 +8,74 @@
 // 2^-16 of its value away from one: a float32 quotient with a Newton step (exact where the quotient is
 // representable, which half-integers are) gives the codes of exact arithmetic.
 //
-// Bound by memory.  A thread moves 8 elements of the key row and the 8 beside them of the value row, for
-// kTokens tokens (independent 16-byte loads or stores); four neighbouring threads share a group, so its
-// maximum takes two shuffles.  Measured (8192 tokens, 8 heads of 128): a division per element takes 23 us
-// to write int8, the multiplication by 1 / s with its step FIGW; reading 32768 such rows takes FIGR us.
+// Bound by memory, if the instructions are few: a thread moves 8 elements of the key row and the 8 beside them
+// of the value row, for kTokens chunks (independent 16-byte loads or stores); four neighbouring lanes share
+// a group, so its maximum takes two shuffles.  Measured for 8192 tokens of 8 heads of 128: writing int8 took
+// 23.4 us with a division per element, 19.2 us with a reciprocal and a Newton step, 15.1 us with packed maxima,
+// whole-warp shuffles and divisions of indexes by multiplication; reading 32768 int8 tokens takes 36 us (5.6 TB/s).
 #include "common.cuh"
 #include "entry.cuh"
 
 namespace w4 {
 namespace kv {
 
+// n / d for n < 2^31: (umulhi(n, mul) + n) >> shift
+struct Divider {
+  uint32_t d, mul;
+  int shift;
+};
+inline Divider divider(uint32_t d) {
+  Divider v{d, 0, 0};
+  while ((1ull << v.shift) < d) ++v.shift;
+  v.mul = static_cast<uint32_t>((((1ull << v.shift) - d) << 32) / d + 1);
+  return v;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) { return (__umulhi(n, v.mul) + n) >> v.shift; }
+
 struct Shape {
-  int64_t T, pages;
-  int heads, dim, page_size, chunks;   // chunks = heads * dim / 8 per token
+  int64_t slots;                       // pages * page_size
+  uint32_t total;                      // chunks of 8 elements in this launch: tokens * heads * dim / 8, below 2^31
+  int heads, dim;
+  Divider chunks, per_head, page_size; // chunks a token, chunks a head, tokens a page
 };
 
-// Cache row index ((page * heads) * page_size + offset, for head 0) of a slot; -1 for none.
-__device__ __forceinline__ int64_t slot_row(int64_t slot, const Shape& s, int32_t* dev_status) {
-  if (slot < 0) return -1;
-  if (slot >= s.pages * s.page_size) { set_status(dev_status, W4_ERR_INVALID_ARG); return -1; }
-  int64_t page;
-  int off;
-  if ((slot >> 32) == 0) {
-    page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(s.page_size);
-    off = static_cast<int>(static_cast<uint32_t>(slot) - static_cast<uint32_t>(page) * s.page_size);
-  } else {
-    page = slot / s.page_size;
-    off = static_cast<int>(slot - page * s.page_size);
+// One thread's chunk: its token, and its place in the cache.
+struct Chunk {
+  uint32_t t, c;                       // token, chunk within it
+  int64_t row;                         // cache row (all heads of all pages counted); -1 for none
+  int d8;                              // chunk within the row
+};
+__device__ __forceinline__ Chunk chunk_of(uint32_t i, const Shape& s, const int64_t* slots, int32_t* dev_status) {
+  Chunk k;
+  k.t = divide(i, s.chunks);
+  k.c = i - k.t * s.chunks.d;
+  const uint32_t head = divide(k.c, s.per_head);
+  k.d8 = static_cast<int>(k.c - head * s.per_head.d);
+  const int64_t slot = __ldg(slots + k.t);
+  k.row = -1;
+  if (slot < 0) return k;
+  if (slot >= s.slots) {
+    set_status(dev_status, W4_ERR_INVALID_ARG);
+    return k;
   }
-  return page * s.heads * s.page_size + off;
+  int64_t page;
+  uint32_t off;
+  if (slot <= 0x7FFFFFFF) {
+    const uint32_t p = divide(static_cast<uint32_t>(slot), s.page_size);
+    off = static_cast<uint32_t>(slot) - p * s.page_size.d;
+    page = p;
+  } else {
+    page = slot / s.page_size.d;
+    off = static_cast<uint32_t>(slot - page * s.page_size.d);
+  }
+  k.row = (page * s.heads + head) * s.page_size.d + off;
+  return k;
 }
 
-constexpr int kTokens = 2;
+constexpr int kTokens = 2;             // chunks a thread works on at once
+constexpr int kThreads = 256;
 
-// rint(x / s) + bias in the low bits of a float of 1.5 * 2^23 and more; s positive and normal, inv = 1 / s
+// rint(x / s) + bias in the low bits of a float of 1.5 * 2^23 and more; s positive and normal, inv near 1 / s
 __device__ __forceinline__ uint32_t quotient(float x, float s, float inv, float bias) {
   const float q = x * inv;
   return __float_as_uint(fmaf(fmaf(-q, s, x), inv, q) + (12582912.f + bias));
@@ -51,29 +85,29 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// 8 bf16 of a group quartet -> codes (2 words int8, 1 word int4) and, in lane 0 of the four, the scale.
+// 8 bf16 of a group quartet -> codes (2 words int8, 1 word int4); returns the scale's bits.  Whole warps only.
 template <int KIND>
 __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&o)[2]) {
   constexpr int kTop = KIND == W4_KV_INT8 ? 127 : 7;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-  const uint32_t quad = 0xFu << ((threadIdx.y * blockDim.x + threadIdx.x) & 28);
-  m = max(m, __shfl_xor_sync(quad, m, 1));
-  m = max(m, __shfl_xor_sync(quad, m, 2));
+  uint32_t pair = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
+  pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 2));
+  const uint32_t m = max(pair & 0xFFFFu, pair >> 16);
   o[0] = KIND == W4_KV_INT4 ? 0x88888888u : 0u;
   o[1] = 0u;
   if (m >= 0x7F80u) return 0x7FC0u;                       // NaN or infinity: codes 0, scale NaN
-  const uint32_t sb = f32_to_bf16_bits(__fdiv_rn(bf16_lo_to_f32(m), static_cast<float>(kTop)));
+  // max / top keeps at least 2^-16 of itself from a bf16 midpoint, so a product rounds as the quotient does
+  const uint32_t sb = f32_to_bf16_bits(bf16_lo_to_f32(m) * (1.f / kTop));
   const float s = bf16_lo_to_f32(sb);
   if (s == 0.f) return 0u;
   uint32_t c[8];                                          // codes (int4: plus 8) in the low bits
   constexpr float kBias = KIND == W4_KV_INT4 ? 8.f : 0.f;
-  if (s >= 0x1p-100f) {
+  if (s >= 0x1p-100f && s <= 0x1p100f) {
     // Rounding max / top to bf16 takes off at most 2^-8 of a scale of 1: |x / s| <= top (1 + 2^-8) < top + 1/2,
     // so nothing has to be clamped.
-    const float inv = __frcp_rn(s);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       c[2 * j] = quotient(bf16_lo_to_f32(w[j]), s, inv, kBias);
@@ -82,8 +116,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&o)[2]) 
   } else {                                                // (a subnormal step can be far below max / top)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = j & 1 ? bf16_hi_to_f32(w[j >> 1]) : bf16_lo_to_f32(w[j >> 1]);
-      c[j] = static_cast<uint32_t>(max(-kTop, min(kTop, __float2int_rn(__fdiv_rn(x, s)))) + static_cast<int>(kBias));
+      const float v = j & 1 ? bf16_hi_to_f32(w[j >> 1]) : bf16_lo_to_f32(w[j >> 1]);
+      c[j] = static_cast<uint32_t>(max(-kTop, min(kTop, __float2int_rn(__fdiv_rn(v, s)))) + static_cast<int>(kBias));
     }
   }
   if (KIND == W4_KV_INT8) {
@@ -95,52 +129,42 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&o)[2]) 
   return sb;
 }
 
+// all lanes of the warp take part; those without a row store nothing
 template <int KIND>
-__device__ __forceinline__ void store_row8(const uint4& x, int64_t row, int dim, int d8, void* cache,
-                                           uint16_t* scales) {
-  if (KIND == W4_KV_BF16) {
-    reinterpret_cast<uint4*>(cache)[row * (dim >> 3) + d8] = x;
-    return;
+__device__ __forceinline__ void store_row8(const uint4& x, const Chunk& k, int dim, void* cache, uint16_t* scales) {
+  const int64_t at = k.row * (dim >> 3) + k.d8;
+  if constexpr (KIND == W4_KV_BF16) {
+    if (k.row >= 0) reinterpret_cast<uint4*>(cache)[at] = x;
+  } else {
+    uint32_t o[2];
+    const uint32_t sb = quantise8<KIND>(x, o);
+    if (k.row < 0) return;
+    if (KIND == W4_KV_INT8) reinterpret_cast<uint2*>(cache)[at] = make_uint2(o[0], o[1]);
+    else reinterpret_cast<uint32_t*>(cache)[at] = o[0];
+    if ((k.d8 & 3) == 0) scales[at >> 2] = static_cast<uint16_t>(sb);
   }
-  uint32_t o[2];
-  const uint32_t sb = quantise8<KIND>(x, o);
-  if (KIND == W4_KV_INT8) reinterpret_cast<uint2*>(cache)[row * (dim >> 3) + d8] = make_uint2(o[0], o[1]);
-  else reinterpret_cast<uint32_t*>(cache)[row * (dim >> 3) + d8] = o[0];
-  if ((d8 & 3) == 0) scales[row * (dim >> 5) + (d8 >> 2)] = static_cast<uint16_t>(sb);
 }
 
-// blockDim = (chunks of a token handled at once, a multiple of 4; tokens), so a group's four threads are
-// neighbours in one warp; what they branch on (the token, its slot) is the same for all four.
 template <int KIND>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 write_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride, int64_t v_stride,
              const int64_t* __restrict__ slots, Shape s, void* k_cache, void* v_cache, uint16_t* k_scales,
              uint16_t* v_scales, int32_t* dev_status) {
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y * kTokens + threadIdx.y;
-  int64_t row0[kTokens];
+  const uint32_t i0 = blockIdx.x * (kThreads * kTokens) + threadIdx.x;
+  Chunk at[kTokens];
+  uint4 kx[kTokens], vx[kTokens];
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int64_t t = t0 + i * static_cast<int>(blockDim.y);
-    row0[i] = t < s.T ? slot_row(__ldg(slots + t), s, dev_status) : -1;
+    const uint32_t n = min(i0 + i * kThreads, s.total - 1);   // (total is a multiple of 4: a group stays whole)
+    at[i] = chunk_of(n, s, slots, dev_status);
+    if (i0 + i * kThreads >= s.total) at[i].row = -1;
+    kx[i] = __ldg(reinterpret_cast<const uint4*>(k + at[i].t * k_stride) + at[i].c);
+    vx[i] = __ldg(reinterpret_cast<const uint4*>(v + at[i].t * v_stride) + at[i].c);
   }
-  const int per_head = s.dim >> 3;
-  for (int c = threadIdx.x; c < s.chunks; c += blockDim.x) {
-    const int head = c / per_head, d8 = c - head * per_head;
-    uint4 kx[kTokens], vx[kTokens];
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      if (row0[i] < 0) continue;
-      const int64_t t = t0 + i * static_cast<int>(blockDim.y);
-      kx[i] = __ldg(reinterpret_cast<const uint4*>(k + t * k_stride) + c);
-      vx[i] = __ldg(reinterpret_cast<const uint4*>(v + t * v_stride) + c);
-    }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      if (row0[i] < 0) continue;
-      const int64_t row = row0[i] + static_cast<int64_t>(head) * s.page_size;
-      store_row8<KIND>(kx[i], row, s.dim, d8, k_cache, k_scales);
-      store_row8<KIND>(vx[i], row, s.dim, d8, v_cache, v_scales);
-    }
+  for (int i = 0; i < kTokens; ++i) {
+    store_row8<KIND>(kx[i], at[i], s.dim, k_cache, k_scales);
+    store_row8<KIND>(vx[i], at[i], s.dim, v_cache, v_scales);
   }
 }
 
@@ -151,9 +175,9 @@ struct Raw {
   uint16_t scale;
 };
 template <int KIND>
-__device__ __forceinline__ Raw<KIND> load_row8(int64_t row, int dim, int d8, const void* cache, const uint16_t* scales) {
+__device__ __forceinline__ Raw<KIND> load_row8(const Chunk& k, int dim, const void* cache, const uint16_t* scales) {
   Raw<KIND> r;
-  const int64_t at = row * (dim >> 3) + d8;
+  const int64_t at = max(k.row, static_cast<int64_t>(0)) * (dim >> 3) + k.d8;   // (row 0 for none: not used)
   if constexpr (KIND == W4_KV_BF16) {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(cache) + at);
     r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
@@ -163,19 +187,18 @@ __device__ __forceinline__ Raw<KIND> load_row8(int64_t row, int dim, int d8, con
   } else {
     r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(cache) + at);
   }
-  if constexpr (KIND != W4_KV_BF16) r.scale = __ldg(scales + row * (dim >> 5) + (d8 >> 2));
+  if constexpr (KIND != W4_KV_BF16) r.scale = __ldg(scales + (at >> 2));
   return r;
 }
 
-// Codes become floats through the low byte of 2^23 (0x4B0000uu is 2^23 + u), which costs a byte permute
-// and a subtraction; code * scale is exact in float32 (at most 7 + 8 bits) and rounded once.
+// A code's bits u = q + bias in the second byte of 2^15 (0x4700uu00) are the float 2^15 + u.  (2^15 + bias) *
+// scale has 17 significant bits at most, so one fused multiply-add gives q * scale exactly; bf16 rounds it once.
 template <int KIND>
 __device__ __forceinline__ uint4 values8(const Raw<KIND>& r) {
   if constexpr (KIND == W4_KV_BF16) {
     return make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
   } else {
-    const float s = bf16_lo_to_f32(r.scale);
-    constexpr float kBias = 8388608.f + (KIND == W4_KV_INT8 ? 128.f : 8.f);
+    const float s = bf16_lo_to_f32(r.scale), off = -(32768.f + (KIND == W4_KV_INT8 ? 128.f : 8.f)) * s;
     uint32_t u[2];                                        // bytes: elements 0..3, 4..7 (int8), even, odd (int4)
     if constexpr (KIND == W4_KV_INT8) {
       u[0] = r.w[0] ^ 0x80808080u;
@@ -189,64 +212,59 @@ __device__ __forceinline__ uint4 values8(const Raw<KIND>& r) {
     for (int j = 0; j < 8; ++j) {
       const uint32_t word = KIND == W4_KV_INT8 ? u[j >> 2] : u[j & 1];
       const int byte = KIND == W4_KV_INT8 ? j & 3 : j >> 1;
-      f[j] = (__uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440 | byte)) - kBias) * s;
+      f[j] = fmaf(__uint_as_float(__byte_perm(word, 0x47000000u, 0x7404 | byte << 4)), s, off);
     }
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   }
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 read_kernel(const int64_t* __restrict__ slots, Shape s, const void* __restrict__ k_cache,
             const void* __restrict__ v_cache, const uint16_t* __restrict__ k_scales,
             const uint16_t* __restrict__ v_scales, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
             int32_t* dev_status) {
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y * kTokens + threadIdx.y;
-  int64_t row0[kTokens];
+  const uint32_t i0 = blockIdx.x * (kThreads * kTokens) + threadIdx.x;
+  Chunk at[kTokens];
+  Raw<KIND> kx[kTokens], vx[kTokens];
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const int64_t t = t0 + i * static_cast<int>(blockDim.y);
-    row0[i] = t < s.T ? slot_row(__ldg(slots + t), s, dev_status) : -1;
+    at[i] = chunk_of(min(i0 + i * kThreads, s.total - 1), s, slots, dev_status);
+    kx[i] = load_row8<KIND>(at[i], s.dim, k_cache, k_scales);
+    vx[i] = load_row8<KIND>(at[i], s.dim, v_cache, v_scales);
   }
-  const int per_head = s.dim >> 3;
-  for (int c = threadIdx.x; c < s.chunks; c += blockDim.x) {
-    const int head = c / per_head, d8 = c - head * per_head;
-    Raw<KIND> kx[kTokens], vx[kTokens];
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      if (row0[i] < 0) continue;
-      const int64_t row = row0[i] + static_cast<int64_t>(head) * s.page_size;
-      kx[i] = load_row8<KIND>(row, s.dim, d8, k_cache, k_scales);
-      vx[i] = load_row8<KIND>(row, s.dim, d8, v_cache, v_scales);
-    }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const int64_t t = t0 + i * static_cast<int>(blockDim.y);
-      if (t >= s.T) continue;
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(k)[t * s.chunks + c] = row0[i] < 0 ? none : values8<KIND>(kx[i]);
-      reinterpret_cast<uint4*>(v)[t * s.chunks + c] = row0[i] < 0 ? none : values8<KIND>(vx[i]);
-    }
+  for (int i = 0; i < kTokens; ++i) {
+    const uint32_t n = i0 + i * kThreads;
+    if (n >= s.total) return;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(k)[n] = at[i].row < 0 ? none : values8<KIND>(kx[i]);
+    reinterpret_cast<uint4*>(v)[n] = at[i].row < 0 ? none : values8<KIND>(vx[i]);
   }
 }
 
-// Shared argument checks; fills the shape and the launch geometry.
+// Shared argument checks; fills the shape (but its total).
 w4_status check(int64_t T, int32_t kind, int32_t heads, int32_t dim, int64_t pages, int32_t page_size,
                 const void* k_cache, const void* v_cache, const uint16_t* k_scales, const uint16_t* v_scales,
-                Shape& s, dim3& block, unsigned& grid) {
+                Shape& s) {
   if (kind != W4_KV_BF16 && kind != W4_KV_INT8 && kind != W4_KV_INT4) return W4_ERR_INVALID_ARG;
   if (T < 0 || heads < 1 || dim < 32 || dim % 32 || pages < 1 || page_size < 1) return W4_ERR_INVALID_ARG;
   if (dim > 1024 || heads > 65536 || T > 0x7FFFFFFFLL || pages > 0x7FFFFFFFLL) return W4_ERR_UNSUPPORTED;
   if (!k_cache || !v_cache || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16)) return W4_ERR_INVALID_ARG;
   if (kind != W4_KV_BF16 && (!k_scales || !v_scales || !aligned_to(k_scales, 2) || !aligned_to(v_scales, 2)))
     return W4_ERR_INVALID_ARG;
-  s = Shape{T, pages, heads, dim, page_size, heads * (dim / 8)};
-  const int bx = s.chunks < 256 ? s.chunks : 256;          // a multiple of 4 either way
-  const int by = 256 / bx;
-  block = dim3(bx, by);
-  grid = static_cast<unsigned>((T + by * kTokens - 1) / (by * kTokens));
+  s.slots = pages * page_size;
+  s.heads = heads;
+  s.dim = dim;
+  s.chunks = divider(heads * (dim / 8));
+  s.per_head = divider(dim / 8);
+  s.page_size = divider(page_size);
   return W4_OK;
 }
+
+// Tokens a launch takes: their chunks are counted in 31 bits, less the last block's overhang.
+inline int64_t tokens_at_once(const Shape& s) { return 0x7FFFF000LL / s.chunks.d; }
+inline unsigned blocks_for(uint32_t total) { return (total + kThreads * kTokens - 1) / (kThreads * kTokens); }
 
 }  // namespace kv
 }  // namespace w4
@@ -260,19 +278,21 @@ w4_status kv_cache_write(const uint16_t* k, const uint16_t* v, int64_t k_stride,
   using namespace w4;
   const EntryRange range("kv_cache_write");
   kv::Shape s;
-  dim3 block;
-  unsigned grid;
-  const w4_status st = kv::check(T, kind, kv_heads, head_dim, pages, page_size, k_cache, v_cache, k_scales, v_scales,
-                                 s, block, grid);
+  const w4_status st = kv::check(T, kind, kv_heads, head_dim, pages, page_size, k_cache, v_cache, k_scales, v_scales, s);
   if (st != W4_OK) return st;
   const int64_t wide = static_cast<int64_t>(kv_heads) * head_dim;
   if (k_stride < wide || v_stride < wide || k_stride % 8 || v_stride % 8) return W4_ERR_INVALID_ARG;
   if (T == 0) return W4_OK;
   if (!k || !v || !slots || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(slots, 8)) return W4_ERR_INVALID_ARG;
-  auto str = static_cast<cudaStream_t>(stream);
   auto fn = kind == W4_KV_BF16 ? kv::write_kernel<W4_KV_BF16>
             : kind == W4_KV_INT8 ? kv::write_kernel<W4_KV_INT8> : kv::write_kernel<W4_KV_INT4>;
-  fn<<<grid, block, 0, str>>>(k, v, k_stride, v_stride, slots, s, k_cache, v_cache, k_scales, v_scales, dev_status);
+  const int64_t most = kv::tokens_at_once(s);
+  for (int64_t t = 0; t < T; t += most) {
+    s.total = static_cast<uint32_t>((T - t < most ? T - t : most) * s.chunks.d);
+    fn<<<kv::blocks_for(s.total), kv::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        k + t * k_stride, v + t * v_stride, k_stride, v_stride, slots + t, s, k_cache, v_cache, k_scales, v_scales,
+        dev_status);
+  }
   return launched();
 }
 
@@ -283,17 +303,18 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
   using namespace w4;
   const EntryRange range("kv_cache_read");
   kv::Shape s;
-  dim3 block;
-  unsigned grid;
-  const w4_status st = kv::check(T, kind, kv_heads, head_dim, pages, page_size, k_cache, v_cache, k_scales, v_scales,
-                                 s, block, grid);
+  const w4_status st = kv::check(T, kind, kv_heads, head_dim, pages, page_size, k_cache, v_cache, k_scales, v_scales, s);
   if (st != W4_OK) return st;
   if (T == 0) return W4_OK;
   if (!k || !v || !slots || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(slots, 8)) return W4_ERR_INVALID_ARG;
-  auto str = static_cast<cudaStream_t>(stream);
   auto fn = kind == W4_KV_BF16 ? kv::read_kernel<W4_KV_BF16>
             : kind == W4_KV_INT8 ? kv::read_kernel<W4_KV_INT8> : kv::read_kernel<W4_KV_INT4>;
-  fn<<<grid, block, 0, str>>>(slots, s, k_cache, v_cache, k_scales, v_scales, k, v, dev_status);
+  const int64_t most = kv::tokens_at_once(s), wide = static_cast<int64_t>(kv_heads) * head_dim;
+  for (int64_t t = 0; t < T; t += most) {
+    s.total = static_cast<uint32_t>((T - t < most ? T - t : most) * s.chunks.d);
+    fn<<<kv::blocks_for(s.total), kv::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        slots + t, s, k_cache, v_cache, k_scales, v_scales, k + t * wide, v + t * wide, dev_status);
+  }
   return launched();
 }
 

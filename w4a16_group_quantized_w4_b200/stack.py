@@ -6,7 +6,9 @@ throughput", section "A repack, not a re-quantization"), are repacked on the dev
 `w4_repack` into int4 codes and bf16 scales, and decode steps then run the four entry points layer
 after layer ("The gap at 26B": 128 experts per layer, 8 active).  The pages give no blocks
 between the MoE layers; a chained step feeds each layer the previous layer's output divided by
-its root mean square (moe_rms_chain, no learned weight), with seeded router logits per layer.
+its root mean square (moe_rms_chain, no learned weight), with seeded router logits per layer.  A decode
+step with attention (decode_step) puts an AttentionBlock in front of every expert layer, the usual
+pre-norm residual block over a paged key/value cache.
 
 Layouts (layer-major, so layer l's weights are contiguous slices):
   gate/up codes [L, E, 2I, H/8] int32, scales [L, E, 2I, H/32] bf16
@@ -27,6 +29,43 @@ class RepackReport:
     off_grid_down: int
     group_m_gate_up: torch.Tensor     # uint8 [L*E*2I, H/32]
     group_m_down: torch.Tensor        # uint8 [L*E*H, I/32]
+
+
+class AttentionBlock:
+    """The attention half of a decoder layer on 4-bit weights, for one new token per sequence:
+
+      h <- h + x;  n = norm(h) in 8-bit rows;  q, k, v = n Wqkv^T;  k, v into the cache;
+      a = attention of q over the cache;  o = a Wo^T;  h <- h + o;  returns norm(h) for the expert layer.
+
+    qkv_codes [(q_heads + 2 kv_heads) D, H/8] with scales [.., H/32], o_codes [H, q_heads D / 8] with
+    scales [.., q_heads D / 32] (layout L1); norms: two bf16 [H] weights or None.  Queries and keys
+    are taken as the projection gives them."""
+
+    def __init__(self, qkv_codes, qkv_scales, o_codes, o_scales, cache: api.KVCache, q_heads: int,
+                 norm_in=None, norm_out=None, softcap: float = 0.0, window: int = 0):
+        _, kv_heads, _, last = cache.k.shape
+        self.dim = last * (8 if cache.kind == "int4" else 1)
+        self.q_heads, self.kv_heads = q_heads, kv_heads
+        if qkv_codes.shape[0] != (q_heads + 2 * kv_heads) * self.dim:
+            raise ValueError("qkv_codes: rows must be (q_heads + 2 kv_heads) * head_dim")
+        if o_codes.shape[1] * 8 != q_heads * self.dim:
+            raise ValueError("o_codes: columns must be q_heads * head_dim / 8")
+        self.qkv, self.o = (qkv_codes, qkv_scales), (o_codes, o_scales)
+        self.cache, self.norm_in, self.norm_out = cache, norm_in, norm_out
+        self.softcap, self.window = softcap, window
+
+    def __call__(self, x, h, page_table, seq_lens, slots, stream=None):
+        """x bf16 [T, H] (the previous layer's output), h bf16 [T, H] the residual stream or None for
+        the first layer; page_table, seq_lens as in kv_cache_attend (the new token counted), slots
+        int64 [T] of the new rows -> (the expert layer's input, h)."""
+        T = x.shape[0]
+        n, ns, h = api.w4_rms_add_q8(x, h, self.norm_in, stream=stream)
+        rows = api.w4a8_linear(n, ns, *self.qkv, stream=stream).unflatten(1, (-1, self.dim))
+        q, k, v = rows.split((self.q_heads, self.kv_heads, self.kv_heads), dim=1)
+        self.cache.write(k, v, slots, stream=stream)
+        a = self.cache.attend(q, page_table, seq_lens, softcap=self.softcap, window=self.window, stream=stream)
+        o = api.w4a16_linear(a.view(T, -1), *self.o, stream=stream)
+        return api.w4_rms_add(o, h, self.norm_out, stream=stream)
 
 
 class MoEStack:
@@ -103,6 +142,21 @@ class MoEStack:
             if l + 1 < self.L:
                 xs.append(api.moe_rms_chain(y, x_next=xb[l], stream=stream))
         return xs, ys
+
+    def decode_step(self, x0, logits, blocks, page_table, seq_lens, slots, norm=None, stream=None,
+                    fused: bool = False):
+        """One decode step through attention and experts: layer l runs blocks[l] (AttentionBlock, each
+        with its own cache; they share page_table, seq_lens and slots) and expert layer l on
+        logits[l] f32 [T, E], around the residual stream that x0 bf16 [T, H] begins.  Returns
+        (norm of the final residual stream with weight `norm`, the stream), both bf16 [T, H]."""
+        if len(blocks) != self.L:
+            raise ValueError(f"blocks: expected {self.L}, got {len(blocks)}")
+        T = x0.shape[0]
+        y, h = x0, None
+        for l, block in enumerate(blocks):
+            x, h = block(y, h, page_table, seq_lens, slots, stream=stream)
+            y = self.layer(l, T, fused)(x, logits[l], stream=stream)
+        return api.w4_rms_add(y, h, norm, stream=stream)
 
     def expert_bytes(self) -> int:
         """Packed bytes of one expert (gate/up + down codes and scales)."""

@@ -92,15 +92,23 @@ __device__ __forceinline__ Span span_of(const Args& a, int b, int cost, bool rep
   return s;
 }
 
-constexpr int kMostBlocks = 4;        // of one SM, in kBlocks
+constexpr int kMostBlocks = 4;        // of one SM, in kShapes
 inline int64_t recs_bytes(int sms) { return (static_cast<int64_t>(sms) * kMostBlocks * sizeof(Rec) + 15) / 16 * 16; }
 
-// [kind][head_dim / 64 - 1]
-constexpr int kTiles[3][4] = {{1, 1, 1, 1}, {2, 1, 1, 1}, {2, 2, 1, 1}};
-constexpr int kStages[3][4] = {{3, 5, 4, 3}, {3, 3, 3, 3}, {3, 3, 3, 3}};
-constexpr int kBlocks[3][4] = {{3, 1, 1, 1}, {3, 3, 2, 2}, {4, 3, 4, 3}};
+// 16-token tiles a stage, stages of a warp's ring and blocks per SM, by [whole][kind][head_dim / 64 - 1]: for
+// long streams, and for items that a block takes whole (short ones: more blocks hide the way to their first
+// bytes, and deep rings would not fill).
+struct Shape {
+  int tiles, stages, blocks;
+};
+constexpr Shape kShapes[2][3][4] = {{{{1, 3, 3}, {1, 5, 1}, {1, 4, 1}, {1, 3, 1}},
+                                     {{2, 3, 3}, {1, 3, 3}, {1, 3, 2}, {1, 3, 2}},
+                                     {{2, 3, 4}, {2, 3, 3}, {1, 3, 4}, {1, 3, 3}}},
+                                    {{{1, 2, 4}, {1, 2, 3}, {1, 2, 2}, {1, 3, 1}},
+                                     {{2, 2, 4}, {1, 2, 3}, {1, 2, 3}, {1, 2, 2}},
+                                     {{2, 2, 4}, {2, 2, 3}, {1, 2, 4}, {1, 2, 3}}}};
 
-template <int KIND, int D>
+template <int KIND, int D, bool WHOLE>
 struct Cfg {
   static constexpr int KW = KIND == W4_KV_BF16 ? 4 : KIND == W4_KV_INT8 ? 2 : 1;   // words per 8 elements
   static constexpr int ROWW = D / 8 * KW;                                           // words per row
@@ -116,9 +124,8 @@ struct Cfg {
   static constexpr int PK = KIND == W4_KV_BF16 ? CPR + 4 : KIND == W4_KV_INT8 ? CPR + 2 : CPR + 1;
   static constexpr int PV = CPR + 1;
   static constexpr int kTileBytes = 16 * 16 * (PK + PV) + (KIND == W4_KV_BF16 ? 0 : 16 * 4 * NG);
-  static constexpr int TT = kTiles[KIND][D / 64 - 1];       // tiles a stage
-  static constexpr int S = kStages[KIND][D / 64 - 1];       // stages of a warp's ring
-  static constexpr int MINB = kBlocks[KIND][D / 64 - 1];    // blocks per SM
+  static constexpr Shape kShape = kShapes[WHOLE][KIND][D / 64 - 1];
+  static constexpr int TT = kShape.tiles, S = kShape.stages, MINB = kShape.blocks;
   static_assert(MINB <= kMostBlocks, "the workspace has room for kMostBlocks an SM");
   static constexpr int kStage = TT * kTileBytes;
   static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
@@ -236,9 +243,14 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int KIND, int D, bool U16>
+// the logarithm of a sum of weights taken relative to m, less the lift
+__device__ __forceinline__ float log_sum(float m, float l, float lift) {
+  return l > 0.f ? (m - lift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int KIND, int D, bool U16, bool WHOLE>
 struct Worker {
-  using C = Cfg<KIND, D>;
+  using C = Cfg<KIND, D, WHOLE>;
   static constexpr bool kBf = KIND == W4_KV_BF16;
   static constexpr int TT = C::TT, NG = C::NG, NV = C::NV, VW = C::VW, VE = C::VE, KW = C::KW;
   static constexpr int kUnitTop = KIND == W4_KV_INT4 ? kScaleTop<KIND> + 24 : kScaleTop<KIND>;   // of the factor's scale
@@ -707,9 +719,10 @@ struct Worker {
   }
 };
 
-template <int KIND, int D, bool U16>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel(const Args a) {
-  using C = Cfg<KIND, D>;
+// WHOLE: block x takes item x as it is.  Otherwise the blocks share the line evenly.
+template <int KIND, int D, bool U16, bool WHOLE>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend_kernel(const Args a) {
+  using C = Cfg<KIND, D, WHOLE>;
   extern __shared__ __align__(16) uint8_t s_ring[];
   auto& s_o = *reinterpret_cast<float(*)[kWarps][kHeads][D + 4]>(s_ring);   // once the stages are done with
   __shared__ uint32_t s_marks[kWarps][C::S];
@@ -718,71 +731,90 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
   __shared__ int64_t s_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_trigger();                                       // (the joining blocks wait for this grid's end)
-  // This block's share of the line.  Every thread adds up its run of sequences; the one whose run holds
-  // the share's first place looks it up in there.
   const int per_seq = a.kv_heads * a.HB;
-  const int run = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = threadIdx.x * run, b1 = min(b0 + run, a.B);
-  int64_t mine = 0;
-  for (int i = b0; i < b1; ++i) mine += span_of(a, i, C::COST, blockIdx.x == 0).line;
-  int64_t upto = mine;
+  int64_t at, end;                                       // this block's share of the line
+  int b, item, at_line;                                  // where it begins: sequence, item of it, place within that
+  Span sp;
+  if constexpr (WHOLE) {
+    b = blockIdx.x / per_seq;
+    item = blockIdx.x - b * per_seq;
+    sp = span_of(a, b, C::COST, item == 0);
+    at = at_line = 0;
+    end = sp.line;
+    if (sp.n == 0) {
+      const int head0 = item / a.HB * a.G + item % a.HB * kHeads, heads = min(kHeads, a.G - item % a.HB * kHeads);
+      const int64_t row0 = static_cast<int64_t>(b) * a.q_heads + head0;
+      uint32_t* row = reinterpret_cast<uint32_t*>(a.out + row0 * D);
+      for (int x = threadIdx.x; x < heads * (D / 2); x += 32 * kWarps) row[x] = 0u;
+      if (a.lse && threadIdx.x < heads) a.lse[row0 + threadIdx.x] = -INFINITY;
+      return;
+    }
+  } else {
+    pdl_trigger();                                       // (the joining blocks wait for this grid's end)
+    // Every thread adds up its run of sequences; the one whose run holds
+    // the share's first place looks it up in there.
+    const int run = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = threadIdx.x * run, b1 = min(b0 + run, a.B);
+    int64_t mine = 0;
+    for (int i = b0; i < b1; ++i) mine += span_of(a, i, C::COST, blockIdx.x == 0).line;
+    int64_t upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-  for (int k = 0; k < kWarps; ++k) {
-    if (k < warp) upto += s_sum[k];
-    total += s_sum[k];
-  }
-  total *= per_seq;
-  // the rows of sequences without tokens
-  for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
-    if (__ldg(a.lens + i) > 0) continue;
-    uint32_t* row = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(i) * a.q_heads * D);
-    for (int x = threadIdx.x; x < a.q_heads * (D / 2); x += 32 * kWarps) row[x] = 0u;
-    if (a.lse)
-      for (int x = threadIdx.x; x < a.q_heads; x += 32 * kWarps) a.lse[static_cast<int64_t>(i) * a.q_heads + x] = -INFINITY;
-  }
-  const int64_t grid = total < gridDim.x ? total : gridDim.x;   // blocks with a share, at least a unit each
-  if (blockIdx.x >= grid) {
-    if (threadIdx.x == 0) a.recs[blockIdx.x].last = -1;
-    return;
-  }
-  int64_t at = total * blockIdx.x / grid;
-  const int64_t end = total * (blockIdx.x + 1) / grid;
-  int64_t from = (upto - mine) * per_seq;
-  if (at >= from && at < upto * per_seq) {
-    int i = b0;
-    for (;; ++i) {
-      const int64_t n = static_cast<int64_t>(span_of(a, i, C::COST, false).line) * per_seq;
-      if (at < from + n) break;
-      from += n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    s_scan[0] = i;
-    s_scan[1] = static_cast<int>(at - from);             // below 2^31: the tokens' limit
-  }
-  __syncthreads();
-  int b = s_scan[0];
-  const int into = s_scan[1];
-  Span sp = span_of(a, b, C::COST, false);
-  int item = into / sp.line;
-  int at_line = into - item * sp.line;                 // place within the item
-  if (threadIdx.x == 0) {
-    // What the joining kernel needs of an item that this block continues and the one before began: the
-    // last block of it.  (An item begins, for that, at its first unit.)
-    Rec rec{b, item, -1};
-    if (at_line > C::COST) {
-      const int64_t unit0 = at - at_line + C::COST, before = total * (blockIdx.x - 1) / grid;
-      if (unit0 >= before) rec.last = static_cast<int>(((unit0 + sp.n) * grid - 1) / total);
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) upto += s_sum[k];
+      total += s_sum[k];
     }
-    a.recs[blockIdx.x] = rec;
+    total *= per_seq;
+    // the rows of sequences without tokens
+    for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
+      if (__ldg(a.lens + i) > 0) continue;
+      uint32_t* row = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(i) * a.q_heads * D);
+      for (int x = threadIdx.x; x < a.q_heads * (D / 2); x += 32 * kWarps) row[x] = 0u;
+      if (a.lse)
+        for (int x = threadIdx.x; x < a.q_heads; x += 32 * kWarps) a.lse[static_cast<int64_t>(i) * a.q_heads + x] = -INFINITY;
+    }
+    const int64_t grid = total < gridDim.x ? total : gridDim.x;   // blocks with a share, at least a unit each
+    if (blockIdx.x >= grid) {
+      if (threadIdx.x == 0) a.recs[blockIdx.x].last = -1;
+      return;
+    }
+    at = total * blockIdx.x / grid;
+    end = total * (blockIdx.x + 1) / grid;
+    int64_t from = (upto - mine) * per_seq;
+    if (at >= from && at < upto * per_seq) {
+      int i = b0;
+      for (;; ++i) {
+        const int64_t n = static_cast<int64_t>(span_of(a, i, C::COST, false).line) * per_seq;
+        if (at < from + n) break;
+        from += n;
+      }
+      s_scan[0] = i;
+      s_scan[1] = static_cast<int>(at - from);             // below 2^31: the tokens' limit
+    }
+    __syncthreads();
+    b = s_scan[0];
+    const int into = s_scan[1];
+    sp = span_of(a, b, C::COST, false);
+    item = into / sp.line;
+    at_line = into - item * sp.line;
+    if (threadIdx.x == 0) {
+      // What the joining kernel needs of an item that this block continues and the one before began: the
+      // last block of it.  (An item begins, for that, at its first unit.)
+      Rec rec{b, item, -1};
+      if (at_line > C::COST) {
+        const int64_t unit0 = at - at_line + C::COST, before = total * (blockIdx.x - 1) / grid;
+        if (unit0 >= before) rec.last = static_cast<int>(((unit0 + sp.n) * grid - 1) / total);
+      }
+      a.recs[blockIdx.x] = rec;
+    }
   }
 
-  Worker<KIND, D, U16> w(a);
+  Worker<KIND, D, U16, WHOLE> w(a);
   w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
   w.marks = s_marks[warp];
   while (true) {
@@ -844,7 +876,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
           *reinterpret_cast<uint2*>(a.out + row * D + d) =
               make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
           if (a.lse && d == 0)
-            a.lse[row] = ll > 0.f ? (mm - (KIND == W4_KV_BF16 ? 0.f : kLift) + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            a.lse[row] = log_sum(mm, ll, KIND == W4_KV_BF16 ? 0.f : kLift);
         } else {
           *reinterpret_cast<float4*>(part + h * D + d) = o;
           if (d == 0) { part[kHeads * D + h] = mm; part[kHeads * D + kHeads + h] = ll; }
@@ -863,74 +895,98 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D>::MINB) attend_kernel
 }
 
 // Joins the parts of split items, in order.  An item is cut where a block's share ends, so the second of
-// its blocks (x) stands for it; y counts its heads.
+// its blocks (x) stands for it; y counts its heads.  Up to kMostGrid parts: first all references and totals,
+// then the sums with many loads in flight (one after the other, 55 parts took 12 us).
+constexpr int kMostGrid = 1024;
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
-  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  __shared__ float s_f[kMostGrid], s_o[4][D], s_m[4], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const Rec rec = a.recs[blockIdx.x];
   const int hk = rec.item / a.HB, hb = rec.item - hk * a.HB, h = blockIdx.y;
   if (rec.last < 0 || hb * kHeads + h >= a.G) return;
-  const int c0 = blockIdx.x - 1, c1 = rec.last;
-  const int64_t row = static_cast<int64_t>(rec.b) * a.q_heads + hk * a.G + hb * kHeads + h;
-  constexpr int V = D / 32;
-  float o[V], m = kLowest, l = 0.f;
+  constexpr int kPart = kHeads * (D + 2), V = D / 32, kBatch = 8;
+  // the first part lies in slot 1 of its block, the others in slot 0 of theirs
+  const int c0 = blockIdx.x - 1, n = rec.last - c0 + 1;
+  auto part = [&](int i) { return a.parts + static_cast<int64_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPart; };
+  float m = kLowest;
+  for (int i = threadIdx.x; i < n; i += 128) {
+    const float pm = part(i)[kHeads * D + h];
+    s_f[i] = pm;
+    m = fmaxf(m, pm);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_m[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float l = 0.f;
+  for (int i = threadIdx.x; i < n; i += 128) {
+    const float f = exp2_fast(s_f[i] - m);
+    s_f[i] = f;
+    l = fmaf(f, part(i)[kHeads * D + kHeads + h], l);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  float o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const float* part = a.parts + static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * kHeads * (D + 2);
-    const float pm = part[kHeads * D + h], pl = part[kHeads * D + kHeads + h];
-    float v[V];
+  for (int i0 = warp; i0 < n; i0 += 4 * kBatch) {
+    float v[kBatch][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = part[h * D + lane + 32 * i];
-    const float mn = fmaxf(m, pm), f = exp2_fast(m - mn), g = exp2_fast(pm - mn);
-    m = mn;
-    l = l * f + pl * g;
+    for (int x = 0; x < kBatch; ++x)
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, v[i] * g);
+      for (int i = 0; i < V; ++i) v[x][i] = i0 + 4 * x < n ? part(i0 + 4 * x)[h * D + lane + 32 * i] : 0.f;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i0 + 4 * x < n) o[i] = fmaf(v[x][i], s_f[i0 + 4 * x], o[i]);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
   __syncthreads();
-  const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float ll = 0.f, f[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) { f[w] = exp2_fast(s_m[w] - mm); ll = fmaf(f[w], s_l[w], ll); }
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) x = fmaf(f[w], s_o[w][d], x);
-    a.out[row * D + d] = f32_to_bf16_bits(x * inv);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = ll > 0.f ? (mm - lift + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t row = static_cast<int64_t>(rec.b) * a.q_heads + hk * a.G + hb * kHeads + h;
+  for (int d = threadIdx.x; d < D; d += 128)
+    a.out[row * D + d] = f32_to_bf16_bits(((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(m, l, lift);
 }
 
-// grid of the attention kernel: every SM filled, or one block a unit where there are fewer
-template <int KIND, int D>
-int grid_of(const Args& a, int sms) {
-  const int64_t units = static_cast<int64_t>(a.B) * a.kv_heads * a.HB *
-                        ((static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit);
-  const int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D>::MINB;
-  return static_cast<int>(units < most ? units : most);
-}
+// How the work is cut.  A block per item, with no scan in front and no join behind it, where no table reaches
+// further than kShort units (257 tokens of 2 heads: 5.5 us against 6.2 when split, and a launch less), or,
+// up to kMiddling units, where there are several items for every block that the SMs hold (2048 items of 4000
+// int8 tokens: 376 us against 403).  Otherwise as many blocks as the SMs hold, or one a unit if fewer.
+constexpr int kShort = 8, kMiddling = 64;
 
-template <int KIND, int D>
-w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
-  const int grid = grid_of<KIND, D>(a, sms);
+template <int KIND, int D, bool WHOLE>
+w4_status launch_mode(const Args& a, int grid, cudaStream_t s) {
   const bool u16 = a.page_size % 16 == 0;
-  auto kernel = u16 ? attend_kernel<KIND, D, true> : attend_kernel<KIND, D, false>;
-  constexpr int kSmem = Cfg<KIND, D>::kSmem;
+  auto kernel = u16 ? attend_kernel<KIND, D, true, WHOLE> : attend_kernel<KIND, D, false, WHOLE>;
+  constexpr int kSmem = Cfg<KIND, D, WHOLE>::kSmem;
   static SmemRaised raised[2];
   if (raise_smem(kernel, kSmem, raised[u16]) != cudaSuccess) return W4_ERR_CUDA;
   kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
-  if (grid == 1) return W4_OK;                           // nothing is split
+  if (WHOLE) return W4_OK;
   const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
   const dim3 joins(grid, a.G < kHeads ? a.G : kHeads);
   return launch_pdl(join_kernel<D>, joins, dim3(128), 0, s, a, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int KIND, int D>
+w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
+  const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * a.HB;
+  const int64_t units = (static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit;
+  int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D, false>::MINB;
+  if (units <= kShort || (units <= kMiddling && items >= 4 * most))
+    return launch_mode<KIND, D, true>(a, static_cast<int>(items), s);
+  most = most < kMostGrid ? most : kMostGrid;
+  return launch_mode<KIND, D, false>(a, static_cast<int>(items * units < most ? items * units : most), s);
 }
 
 template <int KIND>

@@ -108,6 +108,13 @@ constexpr Shape kShapes[2][3][4] = {{{{1, 3, 3}, {1, 5, 1}, {1, 4, 1}, {1, 3, 1}
                                      {{2, 2, 4}, {1, 2, 3}, {1, 2, 3}, {1, 2, 2}},
                                      {{2, 2, 4}, {2, 2, 3}, {1, 2, 4}, {1, 2, 3}}}};
 
+// total * c / grid for c <= grid <= kMostGrid
+constexpr int kMostGrid = 1024;
+__device__ __forceinline__ int64_t share(int64_t total, int c, int grid) {
+  if (total < (1 << 21)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(grid);
+  return total * c / grid;
+}
+
 template <int KIND, int D, bool WHOLE>
 struct Cfg {
   static constexpr int KW = KIND == W4_KV_BF16 ? 4 : KIND == W4_KV_INT8 ? 2 : 1;   // words per 8 elements
@@ -732,7 +739,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const int per_seq = a.kv_heads * a.HB;
-  int64_t at, end;                                       // this block's share of the line
+  int64_t at, end, total = 0;                            // this block's share of the line, the line's length
+  int grid = 1;
   int b, item, at_line;                                  // where it begins: sequence, item of it, place within that
   Span sp;
   if constexpr (WHOLE) {
@@ -764,7 +772,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
     }
     if (lane == 31) s_sum[warp] = upto;
     __syncthreads();
-    int64_t total = 0;
     for (int k = 0; k < kWarps; ++k) {
       if (k < warp) upto += s_sum[k];
       total += s_sum[k];
@@ -778,13 +785,13 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
       if (a.lse)
         for (int x = threadIdx.x; x < a.q_heads; x += 32 * kWarps) a.lse[static_cast<int64_t>(i) * a.q_heads + x] = -INFINITY;
     }
-    const int64_t grid = total < gridDim.x ? total : gridDim.x;   // blocks with a share, at least a unit each
-    if (blockIdx.x >= grid) {
+    grid = static_cast<int>(total < gridDim.x ? total : gridDim.x);   // blocks with a share, at least a unit each
+    if (static_cast<int>(blockIdx.x) >= grid) {
       if (threadIdx.x == 0) a.recs[blockIdx.x].last = -1;
       return;
     }
-    at = total * blockIdx.x / grid;
-    end = total * (blockIdx.x + 1) / grid;
+    at = share(total, blockIdx.x, grid);
+    end = share(total, blockIdx.x + 1, grid);
     int64_t from = (upto - mine) * per_seq;
     if (at >= from && at < upto * per_seq) {
       int i = b0;
@@ -802,17 +809,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
     sp = span_of(a, b, C::COST, false);
     item = into / sp.line;
     at_line = into - item * sp.line;
-    if (threadIdx.x == 0) {
-      // What the joining kernel needs of an item that this block continues and the one before began: the
-      // last block of it.  (An item begins, for that, at its first unit.)
-      Rec rec{b, item, -1};
-      if (at_line > C::COST) {
-        const int64_t unit0 = at - at_line + C::COST, before = total * (blockIdx.x - 1) / grid;
-        if (unit0 >= before) rec.last = static_cast<int>(((unit0 + sp.n) * grid - 1) / total);
-      }
-      a.recs[blockIdx.x] = rec;
-    }
   }
+  const Rec start{b, item, at_line};
+  const int64_t start_at = at;
+  const int start_n = sp.n;
 
   Worker<KIND, D, U16, WHOLE> w(a);
   w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
       }
     }
     at += step;
-    if (at >= end) return;
+    if (at >= end) break;
     at_line = 0;
     if (++item == per_seq) {
       item = 0;
@@ -892,15 +892,27 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
     }
     __syncthreads();
   }
+  if (!WHOLE && threadIdx.x == 0) {
+    // What the joining kernel needs of an item that this block continued and the one before began: the last
+    // block of it.  (An item begins, for that, at its first unit.)
+    Rec rec{start.b, start.item, -1};
+    if (start.last > C::COST) {
+      const int64_t unit0 = start_at - start.last + C::COST;
+      if (unit0 >= share(total, blockIdx.x - 1, grid)) {
+        const int64_t x = unit0 + start_n;               // last + 1 = the least c with total * c >= x * grid
+        rec.last = static_cast<int>((x * grid - 1) / total);
+      }
+    }
+    a.recs[blockIdx.x] = rec;
+  }
 }
 
 // Joins the parts of split items, in order.  An item is cut where a block's share ends, so the second of
 // its blocks (x) stands for it; y counts its heads.  Up to kMostGrid parts: first all references and totals,
 // then the sums with many loads in flight (one after the other, 55 parts took 12 us).
-constexpr int kMostGrid = 1024;
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
-  __shared__ float s_f[kMostGrid], s_o[4][D], s_m[4], s_l[4];
+  __shared__ float s_f[kMostGrid], s_t[kMostGrid], s_o[4][D], s_m[4], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const Rec rec = a.recs[blockIdx.x];
@@ -910,11 +922,20 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   // the first part lies in slot 1 of its block, the others in slot 0 of theirs
   const int c0 = blockIdx.x - 1, n = rec.last - c0 + 1;
   auto part = [&](int i) { return a.parts + static_cast<int64_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPart; };
+  // the first batch of sums is on its way while the factors are found
+  float v[kBatch][V];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[x][i] = i0 + 4 * x < n ? part(i0 + 4 * x)[h * D + lane + 32 * i] : 0.f;
+  };
+  load(warp);
   float m = kLowest;
   for (int i = threadIdx.x; i < n; i += 128) {
-    const float pm = part(i)[kHeads * D + h];
-    s_f[i] = pm;
-    m = fmaxf(m, pm);
+    s_f[i] = part(i)[kHeads * D + h];
+    s_t[i] = part(i)[kHeads * D + kHeads + h];
+    m = fmaxf(m, s_f[i]);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -923,9 +944,8 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   float l = 0.f;
   for (int i = threadIdx.x; i < n; i += 128) {
-    const float f = exp2_fast(s_f[i] - m);
-    s_f[i] = f;
-    l = fmaf(f, part(i)[kHeads * D + kHeads + h], l);
+    s_f[i] = exp2_fast(s_f[i] - m);
+    l = fmaf(s_f[i], s_t[i], l);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -936,11 +956,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
   for (int i0 = warp; i0 < n; i0 += 4 * kBatch) {
-    float v[kBatch][V];
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x)
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[x][i] = i0 + 4 * x < n ? part(i0 + 4 * x)[h * D + lane + 32 * i] : 0.f;
+    if (i0 != warp) load(i0);
 #pragma unroll
     for (int x = 0; x < kBatch; ++x)
 #pragma unroll

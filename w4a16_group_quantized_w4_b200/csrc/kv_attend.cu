@@ -57,7 +57,6 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + at::recs_bytes(device_sm_count()));
   a.dev_status = dev_status;
   a.G = q_heads / kv_heads;
-  a.HB = (a.G + at::kHeads - 1) / at::kHeads;
   a.div_shift = 0;
   while ((1LL << a.div_shift) < page_size) ++a.div_shift;
   a.div_mul = static_cast<uint32_t>((((1ULL << a.div_shift) - page_size) << 32) / page_size + 1);
@@ -68,10 +67,10 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
                                                : at::launch_int4(a, head_dim, s, sms));
 }
 
-// A record and two parts (of a block's first and last item) of kHeads heads for every block of the largest grid.
+// A record and two parts (of a block's first and last item) of 8 heads for every block of the largest grid.
 size_t w4_attend_workspace_bytes(int64_t B, int64_t q_heads, int64_t head_dim, int64_t kv_heads) {
   if (B < 1 || q_heads < 1 || kv_heads < 1 || head_dim < 64 || head_dim > 256) return 0;
   const int sms = w4::device_sm_count();
   const int64_t blocks = static_cast<int64_t>(sms) * w4::at::kMostBlocks;
-  return static_cast<size_t>(w4::at::recs_bytes(sms) + 2 * blocks * w4::at::kHeads * (head_dim + 2) * 4);
+  return static_cast<size_t>(w4::at::recs_bytes(sms) + 2 * blocks * 8 * (head_dim + 2) * 4);
 }

@@ -36,7 +36,6 @@ namespace at {
 
 constexpr int kUnit = 64;             // tokens a work unit
 constexpr int kWarps = 4;
-constexpr int kHeads = 8;             // query heads an item
 constexpr int64_t kMostTokens = 0x7FFFEFFF;   // a sequence's table: token numbers stay below 2^31 past its end
 constexpr float kLowest = -3.0e38f;   // reference before any token: finite, so that masked scores give p = 0
 constexpr float kSlack = 8.f;         // a reference is raised once a score passes it by 2^kSlack
@@ -58,11 +57,11 @@ struct Args {
   int window;
   uint16_t* out;
   float* lse;
-  float* parts;                       // [2 * grid][kHeads * (D + 2)]: sums, references, totals
+  float* parts;                       // [2 * grid][heads * (D + 2)]: sums, references, totals of an item's heads
   Rec* recs;                          // [grid]
   int32_t* dev_status;
   // derived
-  int G, HB;                          // query heads per key/value head, blocks of 8 of them
+  int G, HB;                          // query heads per key/value head, items they make (8 or 16 heads each)
   uint32_t div_mul;                   // token / page_size = (umulhi(token, div_mul) + token) >> div_shift
   int div_shift;
 };
@@ -107,6 +106,9 @@ constexpr Shape kShapes[2][3][4] = {{{{1, 3, 3}, {1, 5, 1}, {1, 4, 1}, {1, 3, 1}
                                     {{{1, 2, 4}, {1, 2, 3}, {1, 2, 2}, {1, 3, 1}},
                                      {{2, 2, 4}, {1, 2, 3}, {1, 2, 3}, {1, 2, 2}},
                                      {{2, 2, 4}, {2, 2, 3}, {1, 2, 4}, {1, 2, 3}}}};
+// Items of 16 heads (more than 8 share a key/value head, head_dim up to 128): keys and values are read from
+// shared memory and widened once for both eights (64 heads over 4, int8, 16384 tokens: 49 us against 58; bf16 56 against 93).
+constexpr Shape kShapes2[3][2] = {{{1, 4, 2}, {1, 3, 2}}, {{2, 3, 2}, {1, 4, 2}}, {{2, 4, 2}, {2, 3, 2}}};
 
 // total * c / grid for c <= grid <= kMostGrid
 constexpr int kMostGrid = 1024;
@@ -115,7 +117,7 @@ __device__ __forceinline__ int64_t share(int64_t total, int c, int grid) {
   return total * c / grid;
 }
 
-template <int KIND, int D, bool WHOLE>
+template <int KIND, int D, int HT, bool WHOLE>
 struct Cfg {
   static constexpr int KW = KIND == W4_KV_BF16 ? 4 : KIND == W4_KV_INT8 ? 2 : 1;   // words per 8 elements
   static constexpr int ROWW = D / 8 * KW;                                           // words per row
@@ -131,9 +133,10 @@ struct Cfg {
   static constexpr int PK = KIND == W4_KV_BF16 ? CPR + 4 : KIND == W4_KV_INT8 ? CPR + 2 : CPR + 1;
   static constexpr int PV = CPR + 1;
   static constexpr int kTileBytes = 16 * 16 * (PK + PV) + (KIND == W4_KV_BF16 ? 0 : 16 * 4 * NG);
-  static constexpr Shape kShape = kShapes[WHOLE][KIND][D / 64 - 1];
+  static constexpr Shape kShape = HT == 2 ? kShapes2[KIND][D / 64 - 1] : kShapes[WHOLE][KIND][D / 64 - 1];
+  static constexpr int kHeads = 8 * HT;                                             // query heads an item
   static constexpr int TT = kShape.tiles, S = kShape.stages, MINB = kShape.blocks;
-  static_assert(MINB <= kMostBlocks, "the workspace has room for kMostBlocks an SM");
+  static_assert(MINB * HT <= kMostBlocks, "the workspace has room for kMostBlocks an SM (of 8 heads)");
   static constexpr int kStage = TT * kTileBytes;
   static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
   static constexpr int kSmem = kWarps * S * kStage > kJoin ? kWarps * S * kStage : kJoin;
@@ -255,9 +258,9 @@ __device__ __forceinline__ float log_sum(float m, float l, float lift) {
   return l > 0.f ? (m - lift + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int KIND, int D, bool U16, bool WHOLE>
+template <int KIND, int D, int HT, bool U16, bool WHOLE>
 struct Worker {
-  using C = Cfg<KIND, D, WHOLE>;
+  using C = Cfg<KIND, D, HT, WHOLE>;
   static constexpr bool kBf = KIND == W4_KV_BF16;
   static constexpr int TT = C::TT, NG = C::NG, NV = C::NV, VW = C::VW, VE = C::VE, KW = C::KW;
   static constexpr int kUnitTop = KIND == W4_KV_INT4 ? kScaleTop<KIND> + 24 : kScaleTop<KIND>;   // of the factor's scale
@@ -269,11 +272,11 @@ struct Worker {
   int lo, hi;                                     // visible tokens of this segment
   uint32_t ring;                                  // this warp's stages in shared memory
   uint32_t* marks;                                // per stage: bit 16 x + i, token i of tile x counts
-  uint32_t qf[D / 16][2];
-  float qb[kBf ? 1 : NG][2];                      // quantised: minus the keys' bias times a group's sum of q
-  float zmul[2];                                  // score -> log2 units, heads 2t and 2t + 1
-  float acc[D / 16][4];
-  float m[2], l[2];
+  uint32_t qf[HT][D / 16][2];
+  float qb[HT][kBf ? 1 : NG][2];                    // quantised: minus the keys' bias times a group's sum of q
+  float zmul[HT][2];                              // score -> log2 units, heads 2t and 2t + 1
+  float acc[HT][D / 16][4];
+  float m[HT][2], l[HT][2];
   int vexp;                                       // quantised: exponent of this output row's unit
 
   __device__ __forceinline__ explicit Worker(const Args& args) : a(args) {
@@ -283,6 +286,11 @@ struct Worker {
   }
 
   __device__ __forceinline__ void load_q(int head0, int heads) {
+#pragma unroll
+    for (int e = 0; e < HT; ++e) load_q8(e, head0 + 8 * e, heads - 8 * e);
+  }
+
+  __device__ __forceinline__ void load_q8(int e, int head0, int heads) {
     const uint16_t* row = a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(head0 + r) * D;
     uint32_t w[NG][4];
 #pragma unroll
@@ -296,9 +304,9 @@ struct Worker {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) { qf[2 * g + s][0] = w[g][2 * s]; qf[2 * g + s][1] = w[g][2 * s + 1]; }
+        for (int s = 0; s < 2; ++s) { qf[e][2 * g + s][0] = w[g][2 * s]; qf[e][2 * g + s][1] = w[g][2 * s + 1]; }
       }
-      zmul[0] = zmul[1] = base;
+      zmul[e][0] = zmul[e][1] = base;
     } else {
       // to fp16 with a power of two per head that brings the largest element to [2^14, 2^15)
       uint32_t mx = 0;
@@ -321,12 +329,12 @@ struct Worker {
           for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              qf[2 * g + s][i] = pack_h2(bf16_lo_to_f32(w[g][2 * s + i]) * up, bf16_hi_to_f32(w[g][2 * s + i]) * up);
+              qf[e][2 * g + s][i] = pack_h2(bf16_lo_to_f32(w[g][2 * s + i]) * up, bf16_hi_to_f32(w[g][2 * s + i]) * up);
         } else {
           // pairs (0, 4), (1, 5), (2, 6), (3, 7), the nibbles' order; those read at bits 4..7 divided by 16
           uint32_t o[4];
           f16_pairs_l1(w[g], up, up * 0.0625f, o);
-          qf[2 * g][0] = o[0]; qf[2 * g][1] = o[1]; qf[2 * g + 1][0] = o[2]; qf[2 * g + 1][1] = o[3];
+          qf[e][2 * g][0] = o[0]; qf[e][2 * g][1] = o[1]; qf[e][2 * g + 1][0] = o[2]; qf[e][2 * g + 1][1] = o[3];
         }
       }
       // sums of the fp16 queries over each group, for heads 2t and 2t + 1
@@ -335,17 +343,17 @@ struct Worker {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&qf[2 * g + i / 2][i & 1]));
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&qf[e][2 * g + i / 2][i & 1]));
           sum += (KIND == W4_KV_INT4 && (i & 1) ? 16.f : 1.f) * (v.x + v.y);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qb[g][0] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
-        qb[g][1] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        qb[e][g][0] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
+        qb[e][g][1] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       }
       const float down = base * pow2f(-f) * (KIND == W4_KV_INT4 ? 16777216.f : 1.f);
-      zmul[0] = __shfl_sync(0xffffffffu, down, 8 * t);
-      zmul[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      zmul[e][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+      zmul[e][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }
   }
 
@@ -448,7 +456,7 @@ struct Worker {
     }
   }
 
-  __device__ __forceinline__ void scores(uint32_t base, float (&s)[TT][4]) const {
+  __device__ __forceinline__ void scores(uint32_t base, float (&s)[HT][TT][4]) const {
 #pragma unroll
     for (int x = 0; x < TT; ++x) {
       const uint32_t ks = base + x * C::kTileBytes + r * (C::PK * 16) + t * (4 * KW);
@@ -459,48 +467,65 @@ struct Worker {
         lds_scales<NG>(ksc[1], ss + 16 * NG);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
+      for (int e = 0; e < HT; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[e][x][i] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         uint32_t k0[KW], k1[KW];
         lds_words<KW>(k0, ks + 16 * g * KW);
         lds_words<KW>(k1, ks + 8 * 16 * C::PK + 16 * g * KW);
+        uint32_t f[2][4];                                // the operands of the group's two products
         if constexpr (kBf) {
-          mma_acc<true>(s[x], k0[0], k1[0], k0[1], k1[1], qf[2 * g][0], qf[2 * g][1]);
-          mma_acc<true>(s[x], k0[2], k1[2], k0[3], k1[3], qf[2 * g + 1][0], qf[2 * g + 1][1]);
-        } else {
-          float c[4] = {qb[g][0], qb[g][1], qb[g][0], qb[g][1]};
-          if constexpr (KIND == W4_KV_INT8) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t x0 = k0[h] ^ 0x80808080u, x1 = k1[h] ^ 0x80808080u;
-              mma_acc<false>(c, key_bytes<0x4140>(x0), key_bytes<0x4140>(x1), key_bytes<0x4342>(x0), key_bytes<0x4342>(x1),
-                             qf[2 * g + h][0], qf[2 * g + h][1]);
-            }
-          } else {
-            mma_acc<false>(c, nib0(k0[0]), nib0(k1[0]), nib1(k0[0]), nib1(k1[0]), qf[2 * g][0], qf[2 * g][1]);
-            mma_acc<false>(c, nib0(k0[0] >> 8), nib0(k1[0] >> 8), nib1(k0[0] >> 8), nib1(k1[0] >> 8), qf[2 * g + 1][0],
-                           qf[2 * g + 1][1]);
+          for (int h = 0; h < 2; ++h) {
+            f[h][0] = k0[2 * h]; f[h][1] = k1[2 * h]; f[h][2] = k0[2 * h + 1]; f[h][3] = k1[2 * h + 1];
           }
-          const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
-          const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
-          const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
-          s[x][0] = fmaf(c[0], s0, s[x][0]);
-          s[x][1] = fmaf(c[1], s0, s[x][1]);
-          s[x][2] = fmaf(c[2], s1, s[x][2]);
-          s[x][3] = fmaf(c[3], s1, s[x][3]);
+        } else if constexpr (KIND == W4_KV_INT8) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x0 = k0[h] ^ 0x80808080u, x1 = k1[h] ^ 0x80808080u;
+            f[h][0] = key_bytes<0x4140>(x0); f[h][1] = key_bytes<0x4140>(x1);
+            f[h][2] = key_bytes<0x4342>(x0); f[h][3] = key_bytes<0x4342>(x1);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x0 = h ? k0[0] >> 8 : k0[0], x1 = h ? k1[0] >> 8 : k1[0];
+            f[h][0] = nib0(x0); f[h][1] = nib0(x1); f[h][2] = nib1(x0); f[h][3] = nib1(x1);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < HT; ++e) {
+          if constexpr (kBf) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_acc<true>(s[e][x], f[h][0], f[h][1], f[h][2], f[h][3], qf[e][2 * g + h][0], qf[e][2 * g + h][1]);
+          } else {
+            float c[4] = {qb[e][g][0], qb[e][g][1], qb[e][g][0], qb[e][g][1]};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_acc<false>(c, f[h][0], f[h][1], f[h][2], f[h][3], qf[e][2 * g + h][0], qf[e][2 * g + h][1]);
+            const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
+            const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
+            const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
+            s[e][x][0] = fmaf(c[0], s0, s[e][x][0]);
+            s[e][x][1] = fmaf(c[1], s0, s[e][x][1]);
+            s[e][x][2] = fmaf(c[2], s1, s[e][x][2]);
+            s[e][x][3] = fmaf(c[3], s1, s[e][x][3]);
+          }
         }
       }
     }
   }
 
   // scores -> weights: masks, the running reference, p in place of s
-  __device__ __forceinline__ void weights(uint32_t mask, float (&s)[TT][4]) {
+  __device__ __forceinline__ void weights(uint32_t mask, int e, float (&s)[TT][4]) {
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][i] *= zmul[i & 1];
+      for (int i = 0; i < 4; ++i) s[x][i] *= zmul[e][i & 1];
     if (a.softcap > 0.f) {
       const float cap = a.softcap * 1.4426950408889634f;
 #pragma unroll
@@ -519,26 +544,26 @@ struct Worker {
     for (int x = 0; x < TT; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[x][i]);
-    if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+    if (__any_sync(0xffffffffu, mx[0] > m[e][0] + kSlack || mx[1] > m[e][1] + kSlack)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
-        const float mn = fmaxf(m[c], mx[c]);
-        const float f = exp2_fast(m[c] - mn);
-        m[c] = mn;
-        l[c] *= f;
+        const float mn = fmaxf(m[e][c], mx[c]);
+        const float f = exp2_fast(m[e][c] - mn);
+        m[e][c] = mn;
+        l[e][c] *= f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) { acc[i][c] *= f; acc[i][2 + c] *= f; }
+        for (int i = 0; i < D / 16; ++i) { acc[e][i][c] *= f; acc[e][i][2 + c] *= f; }
       }
     }
-    const float ref[2] = {kBf ? m[0] : m[0] - kLift, kBf ? m[1] : m[1] - kLift};
+    const float ref[2] = {kBf ? m[e][0] : m[e][0] - kLift, kBf ? m[e][1] : m[e][1] - kLift};
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[x][i] = exp2_fast(s[x][i] - ref[i & 1]);
-        l[i & 1] += s[x][i];
+        l[e][i & 1] += s[x][i];
       }
   }
 
@@ -557,17 +582,20 @@ struct Worker {
     }
   }
 
-  __device__ __forceinline__ void outputs(uint32_t base, uint32_t mask, const float (&s)[TT][4]) {
+  __device__ __forceinline__ void outputs(uint32_t base, uint32_t mask, const float (&s)[HT][TT][4]) {
     if constexpr (kBf) {
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        uint32_t hi_[2], lo_[2];
+        uint32_t hi_[HT][2], lo_[HT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t w = pack_b2(s[x][2 * h], s[x][2 * h + 1]);
-          lo_[h] = transpose8(pack_b2(s[x][2 * h] - bf16_lo_to_f32(w), s[x][2 * h + 1] - bf16_hi_to_f32(w)));
-          hi_[h] = transpose8(w);
-        }
+        for (int e = 0; e < HT; ++e)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float *p = &s[e][x][2 * h];
+            const uint32_t w = pack_b2(p[0], p[1]);
+            lo_[e][h] = transpose8(pack_b2(p[0] - bf16_lo_to_f32(w), p[1] - bf16_hi_to_f32(w)));
+            hi_[e][h] = transpose8(w);
+          }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           uint32_t v[4][VW];
@@ -576,8 +604,11 @@ struct Worker {
           for (int i = 0; i < VW; ++i) {
             const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410), a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
             const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410), a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
-            mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, hi_[0], hi_[1]);
-            mma_acc<true>(acc[j * VE / 2 + i], a0, a1, a2, a3, lo_[0], lo_[1]);
+#pragma unroll
+            for (int e = 0; e < HT; ++e) {
+              mma_acc<true>(acc[e][j * VE / 2 + i], a0, a1, a2, a3, hi_[e][0], hi_[e][1]);
+              mma_acc<true>(acc[e][j * VE / 2 + i], a0, a1, a2, a3, lo_[e][0], lo_[e][1]);
+            }
           }
         }
       }
@@ -622,14 +653,19 @@ struct Worker {
         const float f = exp2_fast(static_cast<float>(vexp - en));
         vexp = en;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < HT * D / 16; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][c] *= f;
+          for (int c = 0; c < 4; ++c) acc[i / (D / 16)][i % (D / 16)][c] *= f;
       }
       const float unit = pow2f(kUnitTop + 127 - vexp);
 #pragma unroll
       for (int x = 0; x < TT; ++x) {
-        const uint32_t p0 = transpose8(pack_h2(s[x][0], s[x][1])), p1 = transpose8(pack_h2(s[x][2], s[x][3]));
+        uint32_t p[HT][2];
+#pragma unroll
+        for (int q = 0; q < HT; ++q) {
+          p[q][0] = transpose8(pack_h2(s[q][x][0], s[q][x][1]));
+          p[q][1] = transpose8(pack_h2(s[q][x][2], s[q][x][3]));
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           uint32_t sv[2], bias[2];
@@ -653,8 +689,10 @@ struct Worker {
                 el[h][2] = value_bytes<0xE6A2>(wa, wb, sv[h], bias[h]);
                 el[h][3] = value_bytes<0xF7B3>(wa, wb, sv[h], bias[h]);
               }
-              mma_acc<false>(acc[j * VE / 2 + 2 * i], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
-              mma_acc<false>(acc[j * VE / 2 + 2 * i + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
+#pragma unroll
+              for (int q = 0; q < HT; ++q) mma_acc<false>(acc[q][j * VE / 2 + 2 * i], el[0][0], el[0][1], el[1][0], el[1][1], p[q][0], p[q][1]);
+#pragma unroll
+              for (int q = 0; q < HT; ++q) mma_acc<false>(acc[q][j * VE / 2 + 2 * i + 1], el[0][2], el[0][3], el[1][2], el[1][3], p[q][0], p[q][1]);
             } else {
 #pragma unroll
               for (int half = 0; half < 2; ++half) {     // elements 0..3, 4..7 of the word
@@ -668,8 +706,10 @@ struct Worker {
                   el[h][2] = h2_fma(nib0(u >> 8), sv[h], bias[h]);
                   el[h][3] = h2_fma(nib1(u >> 8), s1, bias[h]);
                 }
-                mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half], el[0][0], el[0][1], el[1][0], el[1][1], p0, p1);
-                mma_acc<false>(acc[j * VE / 2 + 4 * i + 2 * half + 1], el[0][2], el[0][3], el[1][2], el[1][3], p0, p1);
+  #pragma unroll
+              for (int q = 0; q < HT; ++q) mma_acc<false>(acc[q][j * VE / 2 + 4 * i + 2 * half], el[0][0], el[0][1], el[1][0], el[1][1], p[q][0], p[q][1]);
+  #pragma unroll
+              for (int q = 0; q < HT; ++q) mma_acc<false>(acc[q][j * VE / 2 + 4 * i + 2 * half + 1], el[0][2], el[0][3], el[1][2], el[1][3], p[q][0], p[q][1]);
               }
             }
           }
@@ -680,13 +720,16 @@ struct Worker {
 
   // tiles warp, warp + kWarps, ... from token t0 (a multiple of 16) on, TT of them at once
   __device__ __forceinline__ void walk(int t0, int warp, int head0, int heads) {
-    m[0] = m[1] = kLowest;
-    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int e = 0; e < HT; ++e) {
+      m[e][0] = m[e][1] = kLowest;
+      l[e][0] = l[e][1] = 0.f;
+    }
     vexp = kUnitTop + 1;                             // (2^(kUnitTop + 127 - vexp) stays a float)
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int i = 0; i < HT * D / 16; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+      for (int c = 0; c < 4; ++c) acc[i / (D / 16)][i % (D / 16)][c] = 0.f;
     int tok = t0 + warp * 16;
     if (tok >= hi) return;
     constexpr int kStep = TT * kTileStep;
@@ -712,9 +755,10 @@ struct Worker {
       }
       copy_commit();
       const uint32_t base = ring + st * C::kStage, mask = marks[st];
-      float s[TT][4];
+      float s[HT][TT][4];
       scores(base, s);
-      weights(mask, s);
+#pragma unroll
+      for (int e = 0; e < HT; ++e) weights(mask, e, s[e]);
       outputs(base, mask, s);
       tok += kStep;
       if (tok >= hi) break;
@@ -727,9 +771,10 @@ struct Worker {
 };
 
 // WHOLE: block x takes item x as it is.  Otherwise the blocks share the line evenly.
-template <int KIND, int D, bool U16, bool WHOLE>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend_kernel(const Args a) {
-  using C = Cfg<KIND, D, WHOLE>;
+template <int KIND, int D, int HT, bool U16, bool WHOLE>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, HT, WHOLE>::MINB) attend_kernel(const Args a) {
+  using C = Cfg<KIND, D, HT, WHOLE>;
+  constexpr int kHeads = C::kHeads;
   extern __shared__ __align__(16) uint8_t s_ring[];
   auto& s_o = *reinterpret_cast<float(*)[kWarps][kHeads][D + 4]>(s_ring);   // once the stages are done with
   __shared__ uint32_t s_marks[kWarps][C::S];
@@ -814,7 +859,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
   const int64_t start_at = at;
   const int start_n = sp.n;
 
-  Worker<KIND, D, U16, WHOLE> w(a);
+  Worker<KIND, D, HT, U16, WHOLE> w(a);
   w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
   w.marks = s_marks[warp];
   while (true) {
@@ -834,24 +879,27 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
       // join the warps: head h's reference is the largest of theirs
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int i = 0; i < 2 * HT; ++i) {
+        const int e = i >> 1, c = i & 1;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) w.l[c] += __shfl_xor_sync(0xffffffffu, w.l[c], o);
+        for (int o = 4; o < 32; o <<= 1) w.l[e][c] += __shfl_xor_sync(0xffffffffu, w.l[e][c], o);
         if (w.r == 0) {
-          s_m[warp][2 * w.t + c] = w.m[c];
-          s_l[warp][2 * w.t + c] = w.l[c];
+          s_m[warp][8 * e + 2 * w.t + c] = w.m[e][c];
+          s_l[warp][8 * e + 2 * w.t + c] = w.l[e][c];
         }
       }
       const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop<KIND>);
 #pragma unroll
-      for (int j = 0; j < C::NV; ++j)
+      for (int e = 0; e < HT; ++e)
 #pragma unroll
-        for (int i = 0; i < C::VE / 2; ++i) {
-          const float* o = w.acc[j * C::VE / 2 + i];
-          const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
-          *reinterpret_cast<float2*>(&s_o[warp][2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
-          *reinterpret_cast<float2*>(&s_o[warp][2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
-        }
+        for (int j = 0; j < C::NV; ++j)
+#pragma unroll
+          for (int i = 0; i < C::VE / 2; ++i) {
+            const float* o = w.acc[e][j * C::VE / 2 + i];
+            const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
+            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
+            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
+          }
       __syncthreads();
       const bool whole = take == sp.n;
       // a block continues an item in its slot 0 and begins one in its slot 1
@@ -910,15 +958,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, WHOLE>::MINB) attend
 // Joins the parts of split items, in order.  An item is cut where a block's share ends, so the second of
 // its blocks (x) stands for it; y counts its heads.  Up to kMostGrid parts: first all references and totals,
 // then the sums with many loads in flight (one after the other, 55 parts took 12 us).
-template <int D>
+template <int D, int HT>
 __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   __shared__ float s_f[kMostGrid], s_t[kMostGrid], s_o[4][D], s_m[4], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kHeads = 8 * HT, kPart = kHeads * (D + 2), V = D / 32, kBatch = 8;
   pdl_wait();
   const Rec rec = a.recs[blockIdx.x];
   const int hk = rec.item / a.HB, hb = rec.item - hk * a.HB, h = blockIdx.y;
   if (rec.last < 0 || hb * kHeads + h >= a.G) return;
-  constexpr int kPart = kHeads * (D + 2), V = D / 32, kBatch = 8;
   // the first part lies in slot 1 of its block, the others in slot 0 of theirs
   const int c0 = blockIdx.x - 1, n = rec.last - c0 + 1;
   auto part = [&](int i) { return a.parts + static_cast<int64_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPart; };
@@ -973,36 +1021,47 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(m, l, lift);
 }
 
-// How the work is cut.  A block per item, with no scan in front and no join behind it, where no table reaches
-// further than kShort units (257 tokens of 2 heads: 5.5 us against 6.2 when split, and a launch less), or,
-// up to kMiddling units, where there are several items for every block that the SMs hold (2048 items of 4000
-// int8 tokens: 376 us against 403).  Otherwise as many blocks as the SMs hold, or one a unit if fewer.
-constexpr int kShort = 8, kMiddling = 64;
+// How the work is cut.  A block per item, with no scan in front and no join behind it:
+//   * where no table reaches further than kShort units (64 tokens each; 8 heads of 128, bf16, one sequence: 4.2 us
+//     against 4.9 for 128 tokens, even at 384, 9.0 against 7.6 at 512), a launch less in any case;
+//   * to kLittle units, where the items fill the SMs (512 items of up to 500 tokens: 20.0 us against 25.8);
+//   * to kMiddling units, where there are four items for every block the SMs hold (2048 items of 4000 int8
+//     tokens: 376 us against 403).
+// Otherwise as many blocks as the SMs hold, or one a unit if there are fewer, share the line.
+constexpr int kShort = 6, kLittle = 8, kMiddling = 64;
 
-template <int KIND, int D, bool WHOLE>
+template <int KIND, int D, int HT, bool WHOLE>
 w4_status launch_mode(const Args& a, int grid, cudaStream_t s) {
   const bool u16 = a.page_size % 16 == 0;
-  auto kernel = u16 ? attend_kernel<KIND, D, true, WHOLE> : attend_kernel<KIND, D, false, WHOLE>;
-  constexpr int kSmem = Cfg<KIND, D, WHOLE>::kSmem;
+  auto kernel = u16 ? attend_kernel<KIND, D, HT, true, WHOLE> : attend_kernel<KIND, D, HT, false, WHOLE>;
+  constexpr int kSmem = Cfg<KIND, D, HT, WHOLE>::kSmem;
   static SmemRaised raised[2];
   if (raise_smem(kernel, kSmem, raised[u16]) != cudaSuccess) return W4_ERR_CUDA;
   kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
   if (WHOLE) return W4_OK;
   const float lift = KIND == W4_KV_BF16 ? 0.f : kLift;
-  const dim3 joins(grid, a.G < kHeads ? a.G : kHeads);
-  return launch_pdl(join_kernel<D>, joins, dim3(128), 0, s, a, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+  const dim3 joins(grid, a.G < 8 * HT ? a.G : 8 * HT);
+  return launch_pdl(join_kernel<D, HT>, joins, dim3(128), 0, s, a, lift) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int KIND, int D, int HT>
+w4_status launch_heads(Args a, cudaStream_t s, int sms) {
+  a.HB = (a.G + 8 * HT - 1) / (8 * HT);
+  const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * a.HB;
+  const int64_t units = (static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit;
+  int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D, HT, false>::MINB;
+  if (units <= kShort || (units <= kLittle && items >= most) || (units <= kMiddling && items >= 4 * most))
+    return launch_mode<KIND, D, HT, true>(a, static_cast<int>(items), s);
+  most = most < kMostGrid ? most : kMostGrid;
+  return launch_mode<KIND, D, HT, false>(a, static_cast<int>(items * units < most ? items * units : most), s);
 }
 
 template <int KIND, int D>
 w4_status launch_dim(const Args& a, cudaStream_t s, int sms) {
-  const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * a.HB;
-  const int64_t units = (static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit;
-  int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D, false>::MINB;
-  if (units <= kShort || (units <= kMiddling && items >= 4 * most))
-    return launch_mode<KIND, D, true>(a, static_cast<int>(items), s);
-  most = most < kMostGrid ? most : kMostGrid;
-  return launch_mode<KIND, D, false>(a, static_cast<int>(items * units < most ? items * units : most), s);
+  if constexpr (D <= 128)
+    if (a.G > 8) return launch_heads<KIND, D, 2>(a, s, sms);
+  return launch_heads<KIND, D, 1>(a, s, sms);
 }
 
 template <int KIND>

@@ -329,7 +329,11 @@ w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint1
  *   M >= 0, N >= 1, K >= 32 with K % 32 == 0.
  *   workspace at least w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1) bytes (may be NULL when that
  *             is 0).  Its contents need no preparation; calls sharing it must not overlap on the GPU.
- * Sums inside a group are exact integers; groups are accumulated in float32 in a fixed order.
+ * Up to 64 rows, and for shapes that the tensor-memory kernel of w4a16_linear does not take, sums
+ * inside a group are exact integers and groups are accumulated in float32 in a fixed order.  More rows
+ * of shapes that it takes (N % 128 == 0, K % 64 == 0, K <= 4096, scales 4-byte aligned) go to that kernel
+ * where it is the faster one: every product is exact, the sums are float32.  Either way a call gives the
+ * same bits every time.  N <= 8388480 for more than 32 rows (W4_ERR_UNSUPPORTED beyond).
  */
 w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
                       uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -370,7 +374,7 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
 /*
  * kv_cache_attend -- attention of one new token per sequence over its cached tokens:
  *   out[b, h] = sum_t softmax_t(score) * v_t,  score = cap(scale * q[b, h] . k_t),
- *   cap(z) = softcap * tanh(z / softcap), or z when softcap is 0; the query heads h of
+ *   cap(z) = softcap * tanh(z / softcap), or z when softcap is 0 (else 1e-30 at least); the query heads h of
  *   [g * q_heads / kv_heads, (g + 1) * q_heads / kv_heads) share key/value head g.
  *
  *   q          [B, q_heads, head_dim] bf16 with row stride q_stride elements (a multiple of 8).

@@ -6,14 +6,15 @@ Tolerances (derived, per element):
     within (H / 8 + 16) * 2^-24 relative: partial sums of at most H/8 terms a thread plus the tree.
   * 8-bit rows: |y / s - q| <= 1/2 plus the chain's error times 127.
   * w4a8: group sums are exact, the accumulation of G groups is within (G + 4) * 2^-24 of the sum of
-    the groups' magnitudes, then one bf16 rounding.
+    the groups' magnitudes, then one bf16 rounding.  Many rows go to the tensor-memory kernel, which sums
+    16 exact products a step in float32: within (K / 16) * 2^-23 of the sum of all magnitudes.
 """
 import numpy as np
 import pytest
 import torch
 
 from oracle import bf16, decode
-from w4a16_group_quantized_w4_b200 import api
+from w4a16_group_quantized_w4_b200 import _lib, api
 from tests._util import dev_bf16, dev_u32, host_bf16_bits, host_f64
 
 pytestmark = pytest.mark.gpu
@@ -142,6 +143,29 @@ def test_linear(M, N, K):
                                    (16, 64, 65536)])
 def test_linear_wider(M, N, K):
     check_linear(*linear_case(M, N, K, 11))
+
+
+@pytest.mark.parametrize("M,N,K,off", [(900, 5632, 1024, 0), (1025, 3584, 1088, 0), (900, 5632, 1024, 1)])
+def test_linear_many_rows(M, N, K, off):
+    xq, xs, codes, scales = linear_case(M, N, K, 5)
+    xs[7] = np.nan
+    assert api.w4_workspace_bytes(_lib.W4_OP_LINEAR_8, M, N, K, 1, 1) >= M * K * 2      # the converted rows
+    sd = torch.empty(scales.size + off, dtype=torch.bfloat16, device="cuda")
+    sd = sd[off:].view(N, K // 32).copy_(dev_bf16(scales))
+    y = host_f64(api.w4a8_linear(torch.from_numpy(xq).cuda(), torch.from_numpy(xs).cuda(), dev_u32(codes), sd))
+    assert np.isnan(y[7]).all()
+    keep = np.delete(np.arange(M), 7)
+    w = np.abs(decode.row_values(*_rows_of(codes, scales)))
+    mag = (np.abs(xq[keep].astype(np.float64)) @ w.T) * np.abs(xs[keep].astype(np.float64))[:, None]
+    ref = decode.w4a8_linear(xq[keep], xs[keep], codes, scales)
+    assert (np.abs(y[keep] - ref) <= np.abs(ref) * HALF_BF16 + mag * (K / 16) * 2.0 ** -23).all()
+
+
+def _rows_of(codes, scales):
+    q = np.zeros((codes.shape[0], codes.shape[1] * 8), np.int64)
+    for j in range(8):
+        q[:, j::8] = ((codes >> np.uint32(4 * j)) & np.uint32(15)).astype(np.int64) - 8
+    return q, scales
 
 
 @pytest.mark.parametrize("M", [4, 40, 200])

@@ -14,7 +14,8 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
   if (B < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || head_dim < 1 || pages < 1 || page_size < 1 ||
       table_width < 1 || window < 0)
     return W4_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return W4_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f ||
+      (softcap > 0.f && softcap < 1e-30f)) return W4_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128 && head_dim != 192 && head_dim != 256) return W4_ERR_UNSUPPORTED;
   if (q_heads > 65536 || static_cast<int64_t>(B) * q_heads > 0x7FFFFFFFLL || pages > 0x7FFFFFFFLL ||
       static_cast<int64_t>(table_width) * page_size > at::kMostTokens ||

@@ -140,10 +140,10 @@ struct Cfg {
   static constexpr int kStage = TT * kTileBytes;
   static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
   static constexpr int kSmem = kWarps * S * kStage > kJoin ? kWarps * S * kStage : kJoin;
-  // what beginning an item costs a block (its query, its first loads, its join), in units of tokens:
-  // the time of about 40 KB of the cache
+  // What beginning an item costs a block (its query, its first loads, its join), in units of tokens: about the
+  // time in which an SM's share of the memory bandwidth brings 150 KB, divided among the SM's blocks.
   static constexpr int kUnitBytes = 2 * kUnit * (4 * ROWW + (KIND == W4_KV_BF16 ? 0 : 2 * NG));
-  static constexpr int COST = (40000 + kUnitBytes / 2) / kUnitBytes > 1 ? (40000 + kUnitBytes / 2) / kUnitBytes : 1;
+  static constexpr int COST = 150000 / MINB > kUnitBytes ? (150000 / MINB + kUnitBytes / 2) / kUnitBytes : 1;
 };
 
 template <int W>
@@ -236,6 +236,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// tanh(y ln 2 / 2) = 1 - 2 / (2^y + 1), off by about 2^-22 of 1
+__device__ __forceinline__ float tanh_fast(float y) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(y) + 1.f));
+  return fmaf(-2.f, r, 1.f);
 }
 
 template <bool BF16>
@@ -527,11 +534,12 @@ struct Worker {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[x][i] *= zmul[e][i & 1];
     if (a.softcap > 0.f) {
-      const float cap = a.softcap * 1.4426950408889634f;
+      // cap(z) = softcap tanh(z / softcap), in log2 units on both sides
+      const float cap = a.softcap * 1.4426950408889634f, in = 2.f / a.softcap;
 #pragma unroll
       for (int x = 0; x < TT; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[x][i] = cap * tanhf(s[x][i] / cap);
+        for (int i = 0; i < 4; ++i) s[x][i] = cap * tanh_fast(s[x][i] * in);
     }
     if (mask != ~0u) {
 #pragma unroll

@@ -781,6 +781,10 @@ static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
+                                int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
+                                cudaStream_t stream, int sm_count);
+
 w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int k_div,
                             const uint32_t* codes, const uint16_t* scales, const int32_t* offsets,
                             int E, int64_t rows, int N, int K, int epi, uint16_t* out, void* ws,
@@ -798,6 +802,13 @@ w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int
   w4_launch_a_to_f16(a, a_row_of_pair, kd, a_rows, rows, K, scales, wrows, ws, dev_status, stream,
                      sm_count);
 
+  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count);
+}
+
+// The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16).
+w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
+                                int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
+                                cudaStream_t stream, int sm_count) {
   w4::tm::Args A{};
   A.rowmul = w4_ws_rowmul(ws, rows, K);
   A.rowexp = w4_ws_rowexp(ws, rows, K);

@@ -10,14 +10,22 @@
 //   * The product starts from 0x4B400000, the bits of 1.5 * 2^23: |16 * sum| <= 2^19, so the integer
 //     result read as a float32 is that number plus the sum, exactly, and one subtraction converts it.
 //
-// Two kernels.  Few rows (M <= 32, and the rows fit in shared memory): bound by the weights' bytes, which
+// Three ways.  Few rows (M <= 32, and the rows fit in shared memory): bound by the weights' bytes, which
 // each warp streams through its own ring of stages (TMA tiles) with no block-wide wait; the rows lie in
-// shared memory as ready operands.  More rows: tiles of 128 weight rows by 16 to 64 tokens, 128 k a stage.
+// shared memory as ready operands.  More rows: tiles of 128 weight rows by 16 to 64 tokens, 256 k a stage.
+// Many rows of shapes that fit it: the tensor-memory kernel of tm_gemm.cu on fp16 rows, to which 8-bit rows
+// convert exactly; there a sum runs over products of 24 bits, exact each, in float32 throughout.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "common.cuh"
 #include "entry.cuh"
+#include "tcgen05.cuh"
+
+// from tm_gemm.cu
+bool w4_tm_supported(int N, int K, int epi);
+w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
+                                int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
+                                cudaStream_t stream, int sm_count);
 
 namespace w4 {
 namespace a8 {
@@ -500,11 +508,27 @@ Few few_plan(int64_t M, int64_t KG) {
 
 int many_tile(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
+int64_t many_tiles(int64_t M, int64_t N) {
+  const int BM = many_tile(M);
+  return (M + BM - 1) / BM * ((N + kBN - 1) / kBN);
+}
+
+// Whether the tensor-memory kernel is the faster one for shapes that it takes.  It works in tiles of 128 weight
+// rows by 192 tokens, one an SM at a time, about K * 9 ns each (37 us at K 4096), behind a conversion of about
+// 5 us; the kernel above runs two tiles of 128 by 64 an SM in about K * 11 ns, and can split K where there are
+// fewer tiles than SMs.  Measured, that one first: 509 x 8192 x 2816 67 us and 42; 2048 x 8192 x 4096 308 and
+// 128; 512 x 2816 x 2816 36 and 26; 128 x 14336 x 4096 49 and 35; 64 x 14336 x 4096 35 (stays).
+bool use_tm(int64_t M, int64_t N, int64_t K, int sms) {
+  const double tiles = static_cast<double>(many_tiles(M, N)), tm_tiles = static_cast<double>(N / 128) * ((M + 191) / 192);
+  if (tiles <= sms || !w4_tm_supported(static_cast<int>(N), static_cast<int>(K), W4_EPI_NONE)) return false;
+  const double tm = (tm_tiles > sms ? tm_tiles / sms : 1.0) * K * 9e-9 + 5e-6;
+  const double many = (tiles > 2 * sms ? tiles / (2 * sms) : 1.0) * K * 11e-9 + 4e-6;
+  return tm < many;
+}
+
 // Parts of K: enough to give every SM two blocks, each at least 1024 k long
 int many_splits(int64_t M, int64_t N, int64_t KG, int sms) {
-  const int BM = many_tile(M);
-  const int64_t tiles = (M + BM - 1) / BM * ((N + kBN - 1) / kBN);
-  const int64_t want = 2 * sms / tiles, most = KG / 32;
+  const int64_t want = 2 * sms / many_tiles(M, N), most = KG / 32;
   const int64_t s = want < most ? want : most;
   return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
 }
@@ -588,8 +612,10 @@ w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s
 }  // namespace w4
 
 size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M < 1 || N < 1 || K < 32 || K % 32) return 0;
+  if (M < 1 || N < 1 || K < 32 || K % 32 || N > (1LL << 30) || K > (1LL << 30)) return 0;
   if (w4::a8::few_plan(M, K / 32).S) return 0;
+  // (scales at an odd address keep the call from the tensor-memory kernel: room for either)
+  if (w4::a8::use_tm(M, N, K, w4::device_sm_count())) return w4_tc_workspace_bytes(M, static_cast<int>(K), N);
   const int splits = w4::a8::many_splits(M, N, K / 32, w4::device_sm_count());
   return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
 }
@@ -618,6 +644,12 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   const a8::Few f = a8::few_plan(M, K / 32);
   if (f.S)
     return w4_record_status(f.W == 16 ? a8::launch_few<16>(a, f, SB, sms, s) : a8::launch_few<8>(a, f, SB, sms, s));
+  if (a8::use_tm(M, N, K, sms) && aligned_to(scales, 4)) {
+    w4_launch_a8_to_f16(xq, xs, M, static_cast<int>(K), scales, N, workspace, s, sms);
+    if (cudaGetLastError() != cudaSuccess) return w4_record_status(W4_ERR_CUDA);
+    return w4_record_status(w4_launch_tm_prepared(codes, scales, nullptr, 1, M, static_cast<int>(N), static_cast<int>(K),
+                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms));
+  }
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);
   return w4_record_status(BM == 16 ? a8::launch_many<16>(a, splits, SB, sms, s)

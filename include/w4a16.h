@@ -404,6 +404,25 @@ w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const void* k_cac
                           float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                           void* stream);
 
+/*
+ * w4_packed -- one of the calls above with its arguments in a block, for bindings whose calls cost by the
+ * argument (a Python ctypes call of kv_cache_attend takes 6 us of conversions, one of w4_packed 1 us).
+ *
+ *   entry  a w4_entry.    args  host memory: 64-bit words in the order of the entry point's parameters
+ *          (pointers, integers; `float` parameters as double), led by the number of words that follow.
+ * Same checks, results and errors; W4_ERR_INVALID_ARG for an unknown entry, a wrong number of words, or an
+ * integer that does not fit its parameter.
+ */
+typedef enum {
+  W4_ENTRY_RMS_ADD = 1,
+  W4_ENTRY_RMS_ADD_Q8 = 2,
+  W4_ENTRY_LINEAR_8 = 3,
+  W4_ENTRY_KV_WRITE = 4,
+  W4_ENTRY_KV_READ = 5,
+  W4_ENTRY_KV_ATTEND = 6
+} w4_entry;
+w4_status w4_packed(int32_t entry, const void* args);
+
 /* Workspace bytes an entry point needs for the given sizes (0 when it needs none). */
 size_t w4_workspace_bytes(int32_t op, int64_t M_or_T, int64_t N, int64_t K, int32_t E, int32_t k);
 

@@ -138,3 +138,29 @@ def test_cache_slots_and_bytes():
     assert c.slots(table, torch.tensor([0, 16, 31])).tolist()[::2] == [64, 95]
     words = torch.full((1,), -0x77777778, dtype=torch.int32)
     assert (c.k == words).all() and not c.k_scales.any()
+
+
+def test_packed_calls():
+    """w4_packed: the same answers as the entry points, and its own refusals."""
+    import struct
+    lib = _lib.load()
+
+    def packed(entry, fmt, *values, words=None):
+        return lib.w4_packed(entry, struct.pack("=q" + fmt, len(values) if words is None else words, *values))
+
+    rms_fmt = "QQQqqdQQQ"
+    good = (P, 0, 0, 0, 64, 1e-6, 0, P, 0)                       # no rows: nothing to do
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, *good) == _lib.W4_OK
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, *good, words=8) == BAD
+    assert packed(99, rms_fmt, *good) == BAD and packed(0, rms_fmt, *good) == BAD
+    assert lib.w4_packed(_lib.W4_ENTRY_RMS_ADD, None) == BAD
+    # an integer past its parameter (H is 32 bits), and the entry point's own refusals
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, P, 0, 0, 0, (1 << 32) + 64, 1e-6, 0, P, 0) == BAD
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, P, 0, 0, 4, 12, 1e-6, 0, P, 0) == BAD
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, P, 0, 0, 4, 64, -1.0, 0, P, 0) == BAD
+    assert packed(_lib.W4_ENTRY_RMS_ADD, rms_fmt, P, 0, 0, 4, 32776, 0.0, 0, P, 0) == UNSUP
+    with pytest.raises(_lib.W4Error, match="kv_cache_read failed: W4_ERR_INVALID_ARG"):
+        _lib.kv_read(P, 5, 7, 2, 64, 4, 16, P, P, P, P, P, P, 0, 0)
+    _lib.kv_read(P, 0, _lib.W4_KV_INT8, 2, 64, 4, 16, P, P, P, P, P, P, 0, 0)
+    with pytest.raises(_lib.W4Error):
+        _lib.kv_attend(P, 256, P, P, P, P, 1, P, 3, P, 2, 4, 2, 64, 4, 16, float("nan"), 0.0, 0, P, 0, P, 1 << 20, 0, 0)

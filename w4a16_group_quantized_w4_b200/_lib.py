@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libw4a16.so")
@@ -35,6 +36,13 @@ W4_KV_BF16 = 0
 W4_KV_INT8 = 1
 W4_KV_INT4 = 2
 
+W4_ENTRY_RMS_ADD = 1
+W4_ENTRY_RMS_ADD_Q8 = 2
+W4_ENTRY_LINEAR_8 = 3
+W4_ENTRY_KV_WRITE = 4
+W4_ENTRY_KV_READ = 5
+W4_ENTRY_KV_ATTEND = 6
+
 # name -> (restype, argtypes), mirroring include/w4a16.h
 _P = C.c_void_p
 _I32 = C.c_int32
@@ -61,6 +69,7 @@ SIGNATURES = {
     "kv_cache_read": (_I32, [_P, _I64, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "kv_cache_attend": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _I32,
                                C.c_float, C.c_float, _I32, _P, _P, _P, _SZ, _P, _P]),
+    "w4_packed": (_I32, [_I32, _P]),
     "w4_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32, _I32]),
     "w4_status_str": (C.c_char_p, [_I32]),
     "w4_last_cuda_error": (_I32, []),
@@ -96,6 +105,31 @@ def load(path: str | None = None):
     if path is None:
         _lib = lib
     return lib
+
+
+_NAMES = {W4_ENTRY_RMS_ADD: "w4_rms_add", W4_ENTRY_RMS_ADD_Q8: "w4_rms_add_q8", W4_ENTRY_LINEAR_8: "w4a8_linear",
+          W4_ENTRY_KV_WRITE: "kv_cache_write", W4_ENTRY_KV_READ: "kv_cache_read", W4_ENTRY_KV_ATTEND: "kv_cache_attend"}
+
+
+def _packer(entry: int):
+    """A call of one entry point through w4_packed; raises W4Error like check()."""
+    args = SIGNATURES[_NAMES[entry]][1]
+    block = struct.Struct("=q" + "".join("d" if a is C.c_float else "Q" if a in (_P, _SZ) else "q" for a in args))
+    n = len(args)
+
+    def call(*values):
+        status = load().w4_packed(entry, block.pack(n, *values))
+        if status:
+            raise W4Error(_NAMES[entry], status)
+    return call
+
+
+rms_add = _packer(W4_ENTRY_RMS_ADD)
+rms_add_q8 = _packer(W4_ENTRY_RMS_ADD_Q8)
+linear_8 = _packer(W4_ENTRY_LINEAR_8)
+kv_write = _packer(W4_ENTRY_KV_WRITE)
+kv_read = _packer(W4_ENTRY_KV_READ)
+kv_attend = _packer(W4_ENTRY_KV_ATTEND)
 
 
 def check(fn: str, status: int) -> None:

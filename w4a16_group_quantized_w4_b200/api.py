@@ -419,7 +419,7 @@ def _fits(name, t, dtype, shape, dev):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _rows3(name, t, heads, dim, dev):
@@ -449,7 +449,7 @@ def _scratch(ws, nbytes: int, dev):
     graph keeps it in that graph's own pool."""
     if ws is None:
         if not nbytes:
-            return None, 0, None
+            return 0, 0, None
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         return ws.data_ptr(), nbytes, ws
     _need("ws", ws, torch.uint8, None, dev)
@@ -486,10 +486,7 @@ def w4_rms_add(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, y=No
         y = torch.empty_like(x)
     else:
         _fits("y", y, torch.bfloat16, shape, dev)
-    st = _lib.load().w4_rms_add(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h),
-                                y.data_ptr(), _cur(dev))
-    if st:
-        _lib.check("w4_rms_add", st)
+    _lib.rms_add(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h), y.data_ptr(), _cur(dev))
     return y, x if h is None else h
 
 
@@ -505,10 +502,8 @@ def w4_rms_add_q8(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, q
         q_scale = torch.empty(shape[0], dtype=torch.float32, device=dev)
     else:
         _fits("q_scale", q_scale, torch.float32, shape[:1], dev)
-    st = _lib.load().w4_rms_add_q8(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h),
-                                   q.data_ptr(), q_scale.data_ptr(), _cur(dev))
-    if st:
-        _lib.check("w4_rms_add_q8", st)
+    _lib.rms_add_q8(x.data_ptr(), _ptr(residual), _ptr(weight), shape[0], shape[1], eps, _ptr(h), q.data_ptr(),
+                    q_scale.data_ptr(), _cur(dev))
     return q, q_scale, x if h is None else h
 
 
@@ -529,10 +524,8 @@ def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
     else:
         _fits("y", y, torch.bfloat16, (M, N), dev)
     p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_LINEAR_8, M, N, K, 1, dev.index), dev)
-    st = _lib.load().w4a8_linear(xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M,
-                                 N, K, p, n, _cur(dev))
-    if st:
-        _lib.check("w4a8_linear", st)
+    _lib.linear_8(xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K, p, n,
+                  _cur(dev))
     return y
 
 
@@ -577,11 +570,8 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None, 
     _fits("slots", slots, torch.int64, (T,), dev)
     if dev_status is not None:
         _fits("dev_status", dev_status, torch.int32, (1,), dev)
-    st = _lib.load().kv_cache_write(
-        k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, kind, heads, dim, pages, page_size,
-        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _ptr(dev_status), _cur(dev))
-    if st:
-        _lib.check("kv_cache_write", st)
+    _lib.kv_write(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, kind, heads, dim, pages, page_size,
+                  k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _ptr(dev_status), _cur(dev))
 
 
 @_device_call
@@ -602,11 +592,8 @@ def kv_cache_read(slots, k_cache, v_cache, k_scales=None, v_scales=None, k=None,
         _fits("v", v, torch.bfloat16, want, dev)
     if dev_status is not None:
         _fits("dev_status", dev_status, torch.int32, (1,), dev)
-    st = _lib.load().kv_cache_read(
-        slots.data_ptr(), T, kind, heads, dim, pages, page_size, k_cache.data_ptr(), v_cache.data_ptr(),
-        _ptr(k_scales), _ptr(v_scales), k.data_ptr(), v.data_ptr(), _ptr(dev_status), _cur(dev))
-    if st:
-        _lib.check("kv_cache_read", st)
+    _lib.kv_read(slots.data_ptr(), T, kind, heads, dim, pages, page_size, k_cache.data_ptr(), v_cache.data_ptr(),
+                 _ptr(k_scales), _ptr(v_scales), k.data_ptr(), v.data_ptr(), _ptr(dev_status), _cur(dev))
     return k, v
 
 
@@ -630,7 +617,7 @@ def kv_cache_attend(q, k_cache, v_cache, page_table, seq_lens, k_scales=None, v_
     _fits("page_table", page_table, torch.int32, (B, width), dev)
     _fits("seq_lens", seq_lens, torch.int32, (B,), dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _fits("out", out, torch.bfloat16, shape, dev)
     if lse is not None:
@@ -638,13 +625,11 @@ def kv_cache_attend(q, k_cache, v_cache, page_table, seq_lens, k_scales=None, v_
     if dev_status is not None:
         _fits("dev_status", dev_status, torch.int32, (1,), dev)
     p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_ATTEND, B, q_heads, dim, heads, dev.index), dev)
-    st = _lib.load().kv_cache_attend(
+    _lib.kv_attend(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind,
         page_table.data_ptr(), width, seq_lens.data_ptr(), B, q_heads, heads, dim, pages, page_size,
         dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _ptr(lse), p, n, _ptr(dev_status),
         _cur(dev))
-    if st:
-        _lib.check("kv_cache_attend", st)
     return out
 
 

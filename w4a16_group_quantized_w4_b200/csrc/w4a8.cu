@@ -33,16 +33,6 @@ namespace a8 {
 constexpr uint32_t kMagic = 0x4B400000u;
 constexpr float kMagicF = 12582912.f;
 
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
-  const int n = on ? N : 0;                          // bytes read; the rest of the destination is zeroed
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // 16 * q of the odd (even: after a shift by 4) elements of a code word
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   uint32_t r;
@@ -92,13 +82,47 @@ constexpr int kUnitRows = 16, kUnitGroups = 8;           // a stage: 16 weight r
 constexpr int kCodeBytes = kUnitRows * 16 * kUnitGroups;  // of a stage; its scales follow all stages' codes
 constexpr int kScaleBytes = kUnitRows * 2 * kUnitGroups;
 constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+constexpr int kMostStages = 6;
 
-// W warps, NT blocks of 8 tokens.  SB: bytes a scale copy may take (16, 4 or 2, by the scales' alignment).
-// A block owns a run of weight rows (multiples of 8) in passes of up to W tiles of 16; a pass's tiles
-// times its stages form a line that the warps share evenly, so a tile is cut over two warps at most
-// times (its K is long) and their sums are joined in shared memory, in order.
+// What a warp works on, in order: its share of pass after pass (see few_kernel).
+struct Walk {
+  int W, warp, tiles, KT;
+  int pass, tile, kt, left;        // pass, tile of the pass, its stage, stages left to this warp in the pass
+  __device__ __forceinline__ int pass_tiles(int p) const { return min(W, tiles - p * W); }
+  // goes to the first pass from `pass` on that leaves this warp anything
+  __device__ __forceinline__ bool enter() {
+    for (; pass * W < tiles; ++pass) {
+      const int U = pass_tiles(pass) * KT, u = U < W ? min(warp, U) : U * warp / W;
+      left = (U < W ? min(warp + 1, U) : U * (warp + 1) / W) - u;
+      tile = u / KT;
+      kt = u - tile * KT;
+      if (left > 0) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool next() {
+    if (--left > 0) {
+      if (++kt == KT) {
+        kt = 0;
+        ++tile;
+      }
+      return true;
+    }
+    ++pass;
+    return enter();
+  }
+};
+
+// W warps, NT blocks of 8 tokens.  SB: 16 where the scales come by TMA (their rows are 16-byte aligned), else
+// the bytes of a scale load (4 or 2, by their alignment).
+// A block owns a run of weight rows (multiples of 8) in passes of up to W tiles of 16; a pass's tiles times
+// their stages form a line that the warps share evenly, and the parts that warps have of a tile are joined
+// in shared memory, in order.  Every warp refills its own ring as it frees a stage: one feeding warp for all
+// (a lane per ring) saved instructions but was slower, 14.4 us against 11.7 at M 16, 12.3 against 11.0 at M 1.
 template <int W, int NT, int SB>
-__global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap scales_map, const Args a, int S) {
+__global__ void __launch_bounds__(32 * W, 1)
+few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ CUtensorMap codes8,
+           const __grid_constant__ CUtensorMap scales16, const Args a, int S) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int KT = (a.KG + kUnitGroups - 1) / kUnitGroups;
@@ -108,127 +132,103 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
   // parts follow one another in the order of their stages
   float* red = reinterpret_cast<float*>(xf + static_cast<size_t>(NT) * KT * kUnitGroups * 32);   // [2 W][8 NT][16]
   __shared__ int s_first[W], s_last[W];                                        // a tile's first and last warp
-  __shared__ uint64_t s_bar[W][6];
-  const uint32_t ring = smem_u32(rings) + warp * S * kCodeBytes;               // codes: 128-byte swizzled rows
-  const uint32_t sring = smem_u32(rings) + W * S * kCodeBytes + warp * S * kScaleBytes;
-  uint64_t* bar = s_bar[warp];
-  if (lane < 6) mbar_init(bar + lane, 1);
-  fence_barrier_init();
-  __syncwarp();
+  __shared__ uint64_t s_full[W][kMostStages];
 
   const int c = blockIdx.x;
   const int64_t row_begin = (static_cast<int64_t>(c) * a.eights + min(c, a.more)) * 8;
   const int64_t row_end = min(a.N, row_begin + (a.eights + (c < a.more ? 1 : 0)) * 8);
   const int tiles = static_cast<int>((row_end - row_begin + kUnitRows - 1) / kUnitRows);
-  if (tiles <= 0) return;
-
-  // this warp's place in the sequence of (pass, tile, stage)
-  struct Place {
-    int pass, tile, kt, left;      // tile of the pass, its stage, units left to this warp in the pass
-  };
-  auto pass_tiles = [&](int p) { return min(W, tiles - p * W); };
-  auto enter = [&](Place& p) {     // skips passes that leave this warp nothing
-    for (; p.pass * W < tiles; ++p.pass) {
-      const int U = pass_tiles(p.pass) * KT, u = U < W ? min(warp, U) : U * warp / W;
-      p.left = (U < W ? min(warp + 1, U) : U * (warp + 1) / W) - u;
-      p.tile = u / KT;
-      p.kt = u - p.tile * KT;
-      if (p.left > 0) return true;
-    }
-    return false;
-  };
-  // Codes come as boxes of 8 rows by 128 bytes, zero past the matrix; a box past this block's rows is left
-  // out (what the stage holds there feeds sums that are not written).
-  auto fetch = [&](const Place& p, int st) {
-    const int64_t row0 = row_begin + (p.pass * W + p.tile) * kUnitRows;
-    const int rows = static_cast<int>(min(row_end - row0, static_cast<int64_t>(kUnitRows)));
-    if (lane == 0) {
-      const bool both = rows > 8;
-      mbar_arrive_expect_tx(bar + st, (both ? 2 : 1) * (kCodeBytes / 2 + (SB == 16 ? kScaleBytes / 2 : 0)));
-      uint8_t* dst = rings + (warp * S + st) * kCodeBytes;
-      uint8_t* sdst = rings + W * S * kCodeBytes + (warp * S + st) * kScaleBytes;
-      const int y = static_cast<int>(row0);
-      tma_load_2d(dst, &codes_map, p.kt * 4 * kUnitGroups, y, bar + st);
-      if (both) tma_load_2d(dst + kCodeBytes / 2, &codes_map, p.kt * 4 * kUnitGroups, y + 8, bar + st);
-      if constexpr (SB == 16) {
-        tma_load_2d(sdst, &scales_map, p.kt * kUnitGroups, y, bar + st);
-        if (both) tma_load_2d(sdst + kScaleBytes / 2, &scales_map, p.kt * kUnitGroups, y + 8, bar + st);
-      }
-    }
-    const uint32_t sb = sring + st * kScaleBytes;
-    if constexpr (SB == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 8 * i + (lane >> 2), g = p.kt * kUnitGroups + 2 * (lane & 3);
-        const bool on = row < rows && g < a.KG;
-        copy_async<4>(sb + row * 16 + (lane & 3) * 4, a.scales + (on ? (row0 + row) * a.KG + g : 0), on);
-      }
-    } else if constexpr (SB == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + (lane >> 3), g = p.kt * kUnitGroups + (lane & 7);
-        const bool on = row < rows && g < a.KG;
-        const uint16_t v = on ? ldg_u16(a.scales + (row0 + row) * a.KG + g) : 0;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(sb + row * 16 + (lane & 7) * 2), "h"(v) : "memory");
-      }
-    }
-  };
-
-  Place at{0, 0, 0, 0}, ahead;
-  bool have = enter(at);
-  ahead = at;
-  bool more = have;
-  auto advance = [&](Place& p) {
-    if (--p.left > 0) {
-      if (++p.kt == KT) {
-        p.kt = 0;
-        ++p.tile;
-      }
-      return true;
-    }
-    ++p.pass;
-    return enter(p);
-  };
-  int filled = 0;
-  for (; filled < S - 1; ++filled) {
-    if (more) {
-      fetch(ahead, filled);
-      more = advance(ahead);
-    }
-    if constexpr (SB == 4) copy_commit();
+  if (lane < kMostStages) mbar_init(&s_full[warp][lane], 1);
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&codes16);
+    prefetch_tmap(&codes8);
+    if (SB == 16) prefetch_tmap(&scales16);
   }
+  fence_barrier_init();
+  __syncwarp();
 
-  // the rows as operands, while the first stages are on their way: lane (r, t) of token block b, group g
-  // holds the even and the odd ones of elements 32 g + 8 t .. + 7 of token 8 b + r
-  constexpr int kBatch = 16 / NT;                      // 16 loads in flight a lane
-  for (int g0 = warp; g0 < KT * kUnitGroups; g0 += W * kBatch) {
-    uint2 v[NT][kBatch];
+  // Copies p's stage into place st of the ring of warp p.warp.  Boxes of 16 rows by 128 bytes of codes (8 rows
+  // where the block has no more; a box is zero past the matrix), and 16 rows of scales; rows that are not
+  // this block's feed sums that are not written.
+  auto fetch = [&](const Walk& p, int st) {
+    const int64_t row0 = row_begin + (p.pass * W + p.tile) * kUnitRows;
+    const bool both = row_end - row0 > 8;
+    uint64_t* bar = &s_full[p.warp][st];
+    mbar_arrive_expect_tx(bar, (both ? kCodeBytes : kCodeBytes / 2) + (SB == 16 ? kScaleBytes : 0));
+    tma_load_2d(rings + (p.warp * S + st) * kCodeBytes, both ? &codes16 : &codes8, p.kt * 4 * kUnitGroups,
+                static_cast<int>(row0), bar);
+    if constexpr (SB == 16)
+      tma_load_2d(rings + W * S * kCodeBytes + (p.warp * S + st) * kScaleBytes, &scales16, p.kt * kUnitGroups,
+                  static_cast<int>(row0), bar);
+  };
+
+  // The rows become operands while the first stages are on their way: lane (r, t) of token block b, group g
+  // holds the even and the odd ones of elements 32 g + 8 t .. + 7 of token 8 b + r.  A lane turns 16 bytes of
+  // a row into the operands of two neighbouring lanes.  The first batch of loads goes out before the ring's.
+  constexpr int kBatch = 8 / NT;                       // 8 loads in flight a lane
+  uint4 v[NT][kBatch];
+  auto load_x = [&](int p0) {
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
       const int64_t m = b * 8 + r;
-      const int8_t* row = a.x + (m < a.M ? m : 0) * a.K + t * 8;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i * W;
-        v[b][i] = m < a.M && g < a.KG ? __ldg(reinterpret_cast<const uint2*>(row + g * 32)) : make_uint2(0, 0);
+        const int g = 2 * (p0 + i * W) + (t >> 1);
+        v[b][i] = m < a.M && g < a.KG ? __ldg(reinterpret_cast<const uint4*>(a.x + m * a.K + g * 32) + (t & 1))
+                                      : make_uint4(0, 0, 0, 0);
       }
     }
+  };
+  load_x(warp);
+  Walk at{W, warp, tiles, KT, 0, 0, 0, 0};
+  bool have = at.enter();
+  Walk ahead = at;                                     // the next stage to fetch
+  bool more = have;
+  for (int i = 0; i < S && more; ++i) {
+    if (lane == 0) fetch(ahead, i);
+    more = ahead.next();
+  }
+  for (int p0 = warp; p0 < KT * (kUnitGroups / 2); p0 += W * kBatch) {
+    if (p0 != warp) load_x(p0);
 #pragma unroll
     for (int b = 0; b < NT; ++b)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i * W;
+        const int g = 2 * (p0 + i * W) + (t >> 1);
         if (g < KT * kUnitGroups)
-          xf[(b * KT * kUnitGroups + g) * 32 + lane] = make_uint2(__byte_perm(v[b][i].x, v[b][i].y, 0x6420),
-                                                                  __byte_perm(v[b][i].x, v[b][i].y, 0x7531));
+          *reinterpret_cast<uint4*>(xf + (b * KT * kUnitGroups + g) * 32 + r * 4 + 2 * (t & 1)) =
+              make_uint4(__byte_perm(v[b][i].x, v[b][i].y, 0x6420), __byte_perm(v[b][i].x, v[b][i].y, 0x7531),
+                         __byte_perm(v[b][i].z, v[b][i].w, 0x6420), __byte_perm(v[b][i].z, v[b][i].w, 0x7531));
       }
   }
   __syncthreads();
 
+  // scales of this lane's rows r and r + 8, two groups a word; loaded a stage ahead where they do not come by TMA
+  uint32_t next_sw[2][4];
+  auto load_scales = [&](const Walk& p) {
+    const int64_t row0 = row_begin + (p.pass * W + p.tile) * kUnitRows + r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int g = p.kt * kUnitGroups + 2 * j;
+        const int64_t row = row0 + 8 * h;
+        const uint16_t* at_ = a.scales + row * a.KG + g;
+        const bool on = row < row_end && g < a.KG;
+        if constexpr (SB == 4) next_sw[h][j] = on ? __ldg(reinterpret_cast<const uint32_t*>(at_)) : 0u;
+        else
+          next_sw[h][j] = (on ? ldg_u16(at_) : 0u) | (on && g + 1 < a.KG ? static_cast<uint32_t>(ldg_u16(at_ + 1)) << 16 : 0u);
+      }
+  };
+  if constexpr (SB != 16)
+    if (have) load_scales(at);
+
+  const uint32_t ring = smem_u32(rings) + warp * S * kCodeBytes;             // codes: 128-byte swizzled rows
+  const uint32_t sring = smem_u32(rings) + W * S * kCodeBytes + warp * S * kScaleBytes;
   uint64_t acc[NT][2];
 #pragma unroll
   for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = 0;
-  int st = 0, into = S - 1;
+  int st = 0;
   uint32_t parity = 0;                                 // of the ring's current round
   bool alive = true;                                   // false once a bounded wait ran out: no more waits
   int swz[kUnitGroups];                                // where this lane's word of group g lies in a swizzled row
@@ -236,26 +236,24 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
   for (int g = 0; g < kUnitGroups; ++g) swz[g] = r * 128 + ((g ^ r) << 4) + t * 4;
   const uint32_t xbase = smem_u32(xf) + lane * 8;
   for (int pass = 0; pass * W < tiles; ++pass) {
-    if (have && at.pass == pass) {
-      bool first = at.kt == 0;
-      while (true) {
-        if (alive) alive = mbar_wait_ring(bar + st, parity);
-        if constexpr (SB == 4) {                         // (S is a run-time number: S - 2 groups stay in flight)
-          if (S == 3) copy_wait<1>();
-          else if (S == 4) copy_wait<2>();
-          else if (S == 5) copy_wait<3>();
-          else copy_wait<4>();
+    while (have && at.pass == pass) {
+      // the run of stages that this warp has of a tile
+      const int tile = at.tile, k0 = at.kt, run = min(at.left, KT - k0);
+      uint32_t xk = xbase + k0 * (kUnitGroups * 256);
+      for (int u = 0; u < run; ++u, xk += kUnitGroups * 256) {
+        if (alive) alive = mbar_wait_ring(&s_full[warp][st], parity);
+        const uint32_t base = ring + st * kCodeBytes;
+        uint32_t sw[2][4];
+        if constexpr (SB == 16) {
+          const uint4 s0 = lds128(sring + st * kScaleBytes + r * 16), s1 = lds128(sring + st * kScaleBytes + (r + 8) * 16);
+          sw[0][0] = s0.x; sw[0][1] = s0.y; sw[0][2] = s0.z; sw[0][3] = s0.w;
+          sw[1][0] = s1.x; sw[1][1] = s1.y; sw[1][2] = s1.z; sw[1][3] = s1.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sw[j >> 2][j & 3] = next_sw[j >> 2][j & 3];
+          at.kt = k0 + u + 1;                          // (the next stage's scales, if the run has one)
+          if (u + 1 < run) load_scales(at);
         }
-        __syncwarp();
-        if (more) {
-          fetch(ahead, into);
-          more = advance(ahead);
-        }
-        if constexpr (SB == 4) copy_commit();
-        const uint32_t base = ring + st * kCodeBytes, sbase = sring + st * kScaleBytes;
-        const int kt = at.kt;
-        const uint4 s0 = lds128(sbase + r * 16), s1 = lds128(sbase + (r + 8) * 16);
-        const uint32_t sw[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
 #pragma unroll
         for (int g = 0; g < kUnitGroups; ++g) {
           const uint32_t w0 = lds32(base + swz[g]), w1 = lds32(base + swz[g] + kCodeBytes / 2);
@@ -264,43 +262,46 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
           const uint64_t q1 = twice(g & 1 ? bf16_hi_to_f32(sw[1][g / 2]) : bf16_lo_to_f32(sw[1][g / 2]));
 #pragma unroll
           for (int b = 0; b < NT; ++b) {
-            const uint2 x = lds64(xbase + ((b * KT + kt) * kUnitGroups + g) * 256);
+            const uint2 x = lds64(xk + (b * KT * kUnitGroups + g) * 256);
             uint32_t d[4];
             mma_s8(d, a0, a1, a2, a3, x.x, x.y);
             add_scaled(acc[b][0], d[0], d[1], q0);
             add_scaled(acc[b][1], d[2], d[3], q1);
           }
         }
-        into = st;
+        __syncwarp();                                  // the stage has been read
+        if (more) {
+          if (lane == 0) fetch(ahead, st);
+          more = ahead.next();
+        }
         if (++st == S) {
           st = 0;
           parity ^= 1;
         }
-        const int tile = at.tile;
-        const bool last = kt == KT - 1;
-        have = advance(at);
-        if (!have || at.pass != pass || last) {
-          float* o = red + (warp + tile) * (8 * NT * 16);            // [token][row]
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float lo, hi;
-              halves(acc[b][h], lo, hi);
-              o[(8 * b + 2 * t) * 16 + r + 8 * h] = lo;
-              o[(8 * b + 2 * t + 1) * 16 + r + 8 * h] = hi;
-              acc[b][h] = 0;
-            }
-          if (lane == 0 && first) s_first[tile] = warp;
-          if (lane == 0 && last) s_last[tile] = warp;
-          first = true;
-          if (!have || at.pass != pass) break;
-        }
       }
+      float* o = red + (warp + tile) * (8 * NT * 16);            // [token][row]
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float lo, hi;
+          halves(acc[b][h], lo, hi);
+          o[(8 * b + 2 * t) * 16 + r + 8 * h] = lo;
+          o[(8 * b + 2 * t + 1) * 16 + r + 8 * h] = hi;
+          acc[b][h] = 0;
+        }
+      if (lane == 0 && k0 == 0) s_first[tile] = warp;
+      if (lane == 0 && k0 + run == KT) s_last[tile] = warp;
+      at.kt = k0 + run - 1;
+      at.left -= run - 1;
+      have = at.next();
+      if constexpr (SB != 16)
+        if (have) load_scales(at);
     }
     __syncthreads();
     // a thread sums 4 rows of a token over the tile's parts, in order
-    for (int i = threadIdx.x; i < pass_tiles(pass) * 32 * NT; i += 32 * W) {
+    const int pt = at.pass_tiles(pass);
+    for (int i = threadIdx.x; i < pt * 32 * NT; i += 32 * W) {
       const int quad = i & 3, m = (i >> 2) % (8 * NT), tile = (i >> 2) / (8 * NT);
       const int64_t n = row_begin + (pass * W + tile) * kUnitRows + quad * 4;
       if (m >= a.M || n >= row_end) continue;
@@ -326,9 +327,8 @@ __global__ void __launch_bounds__(32 * W, 1) few_kernel(const __grid_constant__ 
     }
     __syncthreads();
   }
-  if constexpr (SB == 4) copy_wait<0>();
   if (!alive)                                          // copies may still be on their way into this block's memory
-    for (int i = 0; i < S; ++i) mbar_wait_ring(bar + i, parity);
+    for (int i = 0; i < S; ++i) mbar_wait_ring(&s_full[warp][i], parity);
 }
 
 // ----------------------------------------------------------------------------------- more rows
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const Args a, int splits) {
 }
 
 // ----------------------------------------------------------------------------------- dispatch
-constexpr int kSmemMost = 232448 - 1024 - 1024;   // less the static arrays and the ring's alignment
+constexpr int kSmemMost = 232448 - 2048 - 1024;   // less the static arrays and the ring's alignment
 
 // How the few-rows kernel is run: W warps, NT token blocks, S stages; S = 0 where the rows leave no room.
 // 16 warps hide the latency of a warp's chain of products better (M 16, N 14336, K 4096: 17.9 us against
@@ -499,7 +499,7 @@ Few few_plan(int64_t M, int64_t KG) {
   for (f.W = 16; f.W >= 8; f.W -= 8) {
     const int64_t red = f.W * 2 * 8 * f.NT * 16 * 4, S = (kSmemMost - x - red) / (f.W * kStageBytes);
     if (S < 3) continue;
-    f.S = S > 6 ? 6 : static_cast<int>(S);
+    f.S = S > kMostStages ? kMostStages : static_cast<int>(S);
     f.smem = static_cast<int>(x + red + f.W * f.S * kStageBytes);
     return f;
   }
@@ -562,12 +562,13 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
   auto kernel = SB == 16 ? few_kernel<W, NT, 16> : SB >= 4 ? few_kernel<W, NT, 4> : few_kernel<W, NT, 2>;
   static SmemRaised raised[3];
   if (raise_smem(kernel, kSmemMost + 1024, raised[SB == 16 ? 0 : SB >= 4 ? 1 : 2]) != cudaSuccess) return W4_ERR_CUDA;
-  CUtensorMap codes, scales;
-  if (!encode(&codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8, 4 * kUnitGroups, 8,
-              CU_TENSOR_MAP_SWIZZLE_128B))
-    return W4_ERR_CUDA;
-  if (SB != 16) scales = codes;                        // (not used)
-  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kUnitGroups, 8,
+  CUtensorMap codes16, codes8, scales;
+  for (int high : {16, 8})
+    if (!encode(high == 16 ? &codes16 : &codes8, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.N, a.K / 8,
+                4 * kUnitGroups, high, CU_TENSOR_MAP_SWIZZLE_128B))
+      return W4_ERR_CUDA;
+  if (SB != 16) scales = codes16;                      // (not used)
+  else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kUnitGroups, 16,
                    CU_TENSOR_MAP_SWIZZLE_NONE))
     return W4_ERR_CUDA;
   const int64_t R8 = (a.N + 7) / 8;
@@ -575,7 +576,7 @@ w4_status launch_few(const Args& a, const Few& f, int SB, int sms, cudaStream_t 
   Args b = a;
   b.eights = static_cast<int>(R8 / grid);
   b.more = static_cast<int>(R8 % grid);
-  kernel<<<grid, 32 * W, f.smem + 1024, s>>>(codes, scales, b, f.S);
+  kernel<<<grid, 32 * W, f.smem + 1024, s>>>(codes16, codes8, scales, b, f.S);
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

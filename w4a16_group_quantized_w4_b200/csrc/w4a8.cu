@@ -82,7 +82,10 @@ constexpr int kUnitRows = 16, kUnitGroups = 8;           // a stage: 16 weight r
 constexpr int kCodeBytes = kUnitRows * 16 * kUnitGroups;  // of a stage; its scales follow all stages' codes
 constexpr int kScaleBytes = kUnitRows * 2 * kUnitGroups;
 constexpr int kStageBytes = kCodeBytes + kScaleBytes;
-constexpr int kMostStages = 6;
+// Stages of a warp's ring.  Two: 16 warps have 70 KB in flight, which is enough, and more of these boxes (16 rows
+// of 128 bytes each) in flight make the memory slower: the copies alone took 6.9 us with 2 stages and 8.2
+// with 6 for 14336 x 4096 codes, and the kernel at M 1 9.5 and 10.3 us.
+constexpr int kMostStages = 2;
 
 // What a warp works on, in order: its share of pass after pass (see few_kernel).
 struct Walk {
@@ -498,7 +501,7 @@ Few few_plan(int64_t M, int64_t KG) {
   const int64_t x = f.NT * ((KG + kUnitGroups - 1) / kUnitGroups) * kUnitGroups * 256;
   for (f.W = 16; f.W >= 8; f.W -= 8) {
     const int64_t red = f.W * 2 * 8 * f.NT * 16 * 4, S = (kSmemMost - x - red) / (f.W * kStageBytes);
-    if (S < 3) continue;
+    if (S < 2) continue;
     f.S = S > kMostStages ? kMostStages : static_cast<int>(S);
     f.smem = static_cast<int>(x + red + f.W * f.S * kStageBytes);
     return f;

@@ -280,7 +280,8 @@ struct Worker {
   uint32_t ring;                                  // this warp's stages in shared memory
   uint32_t* marks;                                // per stage: bit 16 x + i, token i of tile x counts
   uint32_t qf[HT][D / 16][2];
-  float qb[HT][kBf ? 1 : NG][2];                    // quantised: minus the keys' bias times a group's sum of q
+  float qb[HT][kBf ? 1 : NG][4];                  // quantised: minus the keys' bias times a group's sum of q, as
+                                                  // the products' C operand (heads 2t, 2t + 1, twice)
   float zmul[HT][2];                              // score -> log2 units, heads 2t and 2t + 1
   float acc[HT][D / 16][4];
   float m[HT][2], l[HT][2];
@@ -355,8 +356,8 @@ struct Worker {
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qb[e][g][0] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
-        qb[e][g][1] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        qb[e][g][0] = qb[e][g][2] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
+        qb[e][g][1] = qb[e][g][3] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       }
       const float down = base * pow2f(-f) * (KIND == W4_KV_INT4 ? 16777216.f : 1.f);
       zmul[e][0] = __shfl_sync(0xffffffffu, down, 8 * t);
@@ -509,10 +510,9 @@ struct Worker {
             for (int h = 0; h < 2; ++h)
               mma_acc<true>(s[e][x], f[h][0], f[h][1], f[h][2], f[h][3], qf[e][2 * g + h][0], qf[e][2 * g + h][1]);
           } else {
-            float c[4] = {qb[e][g][0], qb[e][g][1], qb[e][g][0], qb[e][g][1]};
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_acc<false>(c, f[h][0], f[h][1], f[h][2], f[h][3], qf[e][2 * g + h][0], qf[e][2 * g + h][1]);
+            float c[4];
+            mma_f16_16816(c, f[0], qf[e][2 * g][0], qf[e][2 * g][1], qb[e][g]);
+            mma_acc<false>(c, f[1][0], f[1][1], f[1][2], f[1][3], qf[e][2 * g + 1][0], qf[e][2 * g + 1][1]);
             const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
             const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
             const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
@@ -654,9 +654,9 @@ struct Worker {
             if ((w >> 16) < 0x7F80u) e = max(e, w >> 16);
           }
       }
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-      e = max(e, __shfl_xor_sync(0xffffffffu, e, 2)) >> 7;
-      if (__any_sync(0xffffffffu, static_cast<int>(e) > vexp)) {
+      if (__any_sync(0xffffffffu, static_cast<int>(e >> 7) > vexp)) {
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2)) >> 7;
         const int en = max(static_cast<int>(e), vexp);
         const float f = exp2_fast(static_cast<float>(vexp - en));
         vexp = en;

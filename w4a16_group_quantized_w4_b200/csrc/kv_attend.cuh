@@ -191,7 +191,7 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 // Codes as exact fp16 numbers with a bias.  The bits of a code go into the mantissa of a power of two or
-// of a subnormal number; the bias leaves again in float32 (keys: with the product's C operand) or in the
+// of a subnormal number; the bias leaves again in float32 (keys: by products of scales and sums of q) or in the
 // fused multiply by the scale (values), where it must be exact in fp16 after that multiplication.
 //
 // Keys, int8: bytes offset by 128, 0x6400 | u = 1024 + u = 1152 + code.
@@ -245,6 +245,13 @@ __device__ __forceinline__ float tanh_fast(float y) {
   return fmaf(-2.f, r, 1.f);
 }
 
+// D += A(16x8 bf16) * B(8x8 bf16)
+__device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b));
+}
+
 template <bool BF16>
 __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -280,8 +287,10 @@ struct Worker {
   uint32_t ring;                                  // this warp's stages in shared memory
   uint32_t* marks;                                // per stage: bit 16 x + i, token i of tile x counts
   uint32_t qf[HT][D / 16][2];
-  float qb[HT][kBf ? 1 : NG][4];                  // quantised: minus the keys' bias times a group's sum of q, as
-                                                  // the products' C operand (heads 2t, 2t + 1, twice)
+  // Quantised: minus the keys' bias times the sum of q over groups 2t and 2t + 1, for head r, as three bf16 pairs
+  // (their sum has 24 bits).  With a token's scales for the other operand, one more product a part gives what
+  // the biases put into its score.
+  uint32_t qb[HT][3];
   float zmul[HT][2];                              // score -> log2 units, heads 2t and 2t + 1
   float acc[HT][D / 16][4];
   float m[HT][2], l[HT][2];
@@ -345,7 +354,7 @@ struct Worker {
           qf[e][2 * g][0] = o[0]; qf[e][2 * g][1] = o[1]; qf[e][2 * g + 1][0] = o[2]; qf[e][2 * g + 1][1] = o[3];
         }
       }
-      // sums of the fp16 queries over each group, for heads 2t and 2t + 1
+      float bias[2] = {0.f, 0.f};
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = 0.f;
@@ -356,8 +365,13 @@ struct Worker {
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qb[e][g][0] = qb[e][g][2] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t);
-        qb[e][g][1] = qb[e][g][3] = -kKeyBias<KIND> * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        if (g / 2 == t) bias[g & 1] = -kKeyBias<KIND> * sum;
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        qb[e][i] = pack_b2(bias[0], bias[1]);
+        bias[0] -= bf16_lo_to_f32(qb[e][i]);
+        bias[1] -= bf16_hi_to_f32(qb[e][i]);
       }
       const float down = base * pow2f(-f) * (KIND == W4_KV_INT4 ? 16777216.f : 1.f);
       zmul[e][0] = __shfl_sync(0xffffffffu, down, 8 * t);
@@ -470,14 +484,20 @@ struct Worker {
       const uint32_t ks = base + x * C::kTileBytes + r * (C::PK * 16) + t * (4 * KW);
       const uint32_t ss = base + x * C::kTileBytes + 256 * (C::PK + C::PV) + r * (2 * NG);
       uint32_t ksc[2][kBf ? 1 : NG / 2];
-      if constexpr (!kBf) {
-        lds_scales<NG>(ksc[0], ss);
-        lds_scales<NG>(ksc[1], ss + 16 * NG);
-      }
 #pragma unroll
       for (int e = 0; e < HT; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[e][x][i] = 0.f;
+      if constexpr (!kBf) {
+        lds_scales<NG>(ksc[0], ss);
+        lds_scales<NG>(ksc[1], ss + 16 * NG);
+        const uint32_t pair = 4 * min(t, NG / 2 - 1);      // (beyond the groups the other operand is 0)
+        const uint32_t a0 = lds32(ss + pair), a1 = lds32(ss + 16 * NG + pair);
+#pragma unroll
+        for (int e = 0; e < HT; ++e)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) mma_k8(s[e][x], a0, a1, qb[e][i]);
+      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         uint32_t k0[KW], k1[KW];
@@ -511,7 +531,7 @@ struct Worker {
               mma_acc<true>(s[e][x], f[h][0], f[h][1], f[h][2], f[h][3], qf[e][2 * g + h][0], qf[e][2 * g + h][1]);
           } else {
             float c[4];
-            mma_f16_16816(c, f[0], qf[e][2 * g][0], qf[e][2 * g][1], qb[e][g]);
+            mma_f16_16816(c, f[0], qf[e][2 * g][0], qf[e][2 * g][1], {0.f, 0.f, 0.f, 0.f});
             mma_acc<false>(c, f[1][0], f[1][1], f[1][2], f[1][3], qf[e][2 * g + 1][0], qf[e][2 * g + 1][1]);
             const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
             const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);

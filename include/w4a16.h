@@ -393,7 +393,11 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  *   head_dim 64, 128, 192 or 256 (W4_ERR_UNSUPPORTED otherwise); any page_size >= 1;
  *   q_heads % kv_heads == 0; table_width * page_size < 2^31 - 4096 and, times q_heads, below
  *   2^36; pages * kv_heads * page_size < 2^32 (W4_ERR_UNSUPPORTED beyond).
- * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.
+ * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.  Weights enter the sum over
+ * bf16 values with 16 bits; over int8 and int4 values weights and scaled values enter it in fp16, rounded to
+ * 11 bits.  Weights below 2^-20 of the sequence's largest keep fewer; so do values, an error of 2^-20 of the
+ * largest scale that meets the same output element being possible, and, against an int8 or int4 cache, elements
+ * of q below 2^-24 of their head's largest.
  * Rows of the cache that no sequence's (windowed) length covers are never looked at.
  */
 w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,

@@ -129,7 +129,7 @@ def test_slots_past_the_cache_are_reported_and_dropped(kind):
 class Seqs:
     """Sequences of given lengths in a paged cache with shuffled pages, and their float64 rows."""
 
-    def __init__(self, lens, heads, dim, page, kind, seed, junk=True, size=1.0):
+    def __init__(self, lens, heads, dim, page, kind, seed, junk=True, size=1.0, spread=0):
         r = np.random.RandomState(seed)
         self.lens, self.heads, self.dim, self.kind = lens, heads, dim, kind
         need = [-(-n // page) for n in lens]
@@ -155,7 +155,8 @@ class Seqs:
             pos = np.arange(n)
             slots.append(self.table[b, pos // page].astype(np.int64) * page + pos % page)
             ks.append(rows(r, n, heads, dim))
-            vs.append(bf16.from_f64(size * bf16.to_f64(rows(r, n, heads, dim))))
+            each = 2.0 ** np.random.RandomState(n).randint(-spread, spread + 1, (n, 1, 1))
+            vs.append(bf16.from_f64(size * each * bf16.to_f64(rows(r, n, heads, dim))))
         slots = np.concatenate(slots)
         k, v = np.concatenate(ks), np.concatenate(vs)
         if len(slots):
@@ -180,7 +181,7 @@ class Seqs:
             c = q
         return c.astype(np.float64) * np.repeat(s, 32, axis=-1)
 
-    def check(self, q_heads, seed=0, scale=None, softcap=0.0, window=0, strided=False, q=None):
+    def check(self, q_heads, seed=0, scale=None, softcap=0.0, window=0, strided=False, q=None, floor=0.0):
         r = np.random.RandomState(seed)
         B = len(self.lens)
         q = bf16.from_f64(r.randn(B, q_heads, self.dim)) if q is None else q
@@ -204,6 +205,8 @@ class Seqs:
                                                         softcap, window)
                 dz = (self.dim + 16) * 2.0 ** -24 * abs(scale) * peak + 2.0 ** -20 * max(1.0, softcap)
                 tol = np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -9 + 2 * dz) + 2.0 ** -31 * vsum
+                if floor:
+                    tol = tol + floor * np.abs(self.v[b][:, h // G]).max()
                 assert (np.abs(got[b, h] - ref) <= tol).all(), (b, h, np.abs(got[b, h] - ref).max())
                 if self.lens[b]:
                     assert abs(lse[b, h] - ref_lse) <= 2.0 ** -11 + 2 * dz + abs(ref_lse) * 2.0 ** -23
@@ -243,6 +246,38 @@ def test_long_sequences_split_and_joined(kind, lens, dim, page):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,q_heads,lens,page", [(1, 9, [3000], 16), (1, 16, [1, 2049, 0, 700], 7), (2, 40, [4100, 65], 48),
+                                                     (1, 33, [1800], 32)])
+def test_many_heads_over_long_sequences(kind, dim, heads, q_heads, lens, page):
+    """Items of 16 heads, cut and joined, the last of them with fewer."""
+    Seqs(lens, heads, dim, page, kind, q_heads).check(q_heads, scale=0.2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [192, 256])
+def test_many_heads_of_wide_rows(kind, dim):
+    Seqs([1500, 90], 1, dim, 16, kind, dim).check(20, scale=0.2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,softcap", [(700, 0.0), (1999, 3.0), (2049, 0.0)])
+@pytest.mark.parametrize("q_heads", [4, 12])
+def test_window_over_long_sequences(kind, window, softcap, q_heads):
+    Seqs([2000, 5, 3333, 2049], 1, 128, 16, kind, 9).check(q_heads, softcap=softcap, window=window)
+
+
+# tables of 8 units over 600 items, and of 20 units over 2500: a block takes an item whole
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,longest,heads,q_heads,dim", [(150, 496, 4, 4, 64), (75, 480, 8, 80, 64), (320, 1264, 8, 8, 64)])
+def test_items_taken_whole(kind, B, longest, heads, q_heads, dim):
+    r = np.random.RandomState(B)
+    lens = [int(n) for n in np.minimum(longest, 2 ** r.uniform(0, np.log2(longest), B))]
+    lens[3], lens[5] = longest, 0
+    Seqs(lens, heads, dim, 16, kind, 4).check(q_heads)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_many_sequences(kind):
     r = np.random.RandomState(8)
     lens = [int(n) for n in r.randint(0, 90, 300)]
@@ -259,6 +294,16 @@ def test_sharp_and_flat_softmax(kind, scale):
 @pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 40])
 def test_values_of_unlike_sizes(kind, size):
     Seqs([200, 31], 2, 64, 16, kind, 7, size=size).check(4)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("scale", [0.125, 4.0])
+def test_tokens_of_unlike_sizes(kind, scale):
+    """Tokens whose values lie 2^20 apart: a large one of no weight must not cost a small one its bits.  Below
+    the normal range scaled fp16 values are off by 2^-21 (int8) or 2^-20 (int4) of the largest scale, and a scale
+    is at most the largest value of its group over 127 or 7: 2^-27 or 2^-22 of the largest value."""
+    floor = {"bf16": 0.0, "int8": 2.0 ** -27, "int4": 2.0 ** -22}[kind]
+    Seqs([200, 31, 1500], 2, 64, 16, kind, 7, spread=10).check(4, scale=scale, floor=floor)
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -164,3 +164,17 @@ def test_packed_calls():
     _lib.kv_read(P, 0, _lib.W4_KV_INT8, 2, 64, 4, 16, P, P, P, P, P, P, 0, 0)
     with pytest.raises(_lib.W4Error):
         _lib.kv_attend(P, 256, P, P, P, P, 1, P, 3, P, 2, 4, 2, 64, 4, 16, float("nan"), 0.0, 0, P, 0, P, 1 << 20, 0, 0)
+
+
+def test_first_tensor_by_its_name():
+    """Every argument may be named, the first among them."""
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    for call in (lambda: api.w4_rms_add(x=x), lambda: api.w4_rms_add_q8(x=x),
+                 lambda: api.w4a8_linear(xq=x, xs=x, codes=x, scales=x),
+                 lambda: api.kv_cache_write(k=x, v=x, slots=x, k_cache=x, v_cache=x),
+                 lambda: api.kv_cache_read(slots=x, k_cache=x, v_cache=x),
+                 lambda: api.kv_cache_attend(q=x, k_cache=x, v_cache=x, page_table=x, seq_lens=x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError, match="x: expected a torch.Tensor"):
+        api.w4_rms_add()

@@ -382,22 +382,25 @@ def _device_call(fn):
     """Runs fn with the current device and stream set as its arguments ask: on `stream` when one is
     given (allocations included, so that a returned tensor belongs to that stream), otherwise on
     the current stream of the first tensor's device, whichever device is current."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor):
-            raise TypeError(f"{fn.__name__}: expected a torch.Tensor first")
+            raise TypeError(f"{name}: expected a torch.Tensor")
         if not first.is_cuda:
-            raise ValueError(f"{fn.__name__}: tensors must live on a CUDA device")
+            raise ValueError(f"{name}: must live on a CUDA device")
         dev = first.device
         if stream is not None:
             if stream.device != dev:
                 raise ValueError(f"stream: expected device {dev}, got {stream.device}")
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if dev.index != torch.cuda.current_device():
             with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 

@@ -185,7 +185,7 @@ def test_slots_of_positions_outside_the_table():
     table = torch.tensor([[2, 0], [1, 3], [0, -1], [3, 9]], dtype=torch.int32)
     at = lambda *p: cache.slots(table, torch.tensor(p, dtype=torch.int32)).tolist()
     assert at(5, 16, -1, 0) == [37, 48, -1, 48]
-    past = at(32, 1 << 30, 16, 17)
+    past = at(32, 1 << 30, 4096, 17)
     assert all(s >= 4 * 16 for s in past)                   # reported and dropped by a write
     with pytest.raises(ValueError):
         cache.slots(table[:, :0], torch.zeros(4, dtype=torch.int32))

@@ -671,8 +671,8 @@ class KVCache:
 
     def slots(self, page_table, positions):
         """Slots int64 [B] of one position per sequence (int tensor [B]; negative positions stay
-        padded): where a decode step writes its new rows.  A position that the table does not cover, or
-        whose page is negative, gets a slot past the cache, which a write reports and drops."""
+        padded): where a decode step writes its new rows.  A position on a negative page stays padded too;
+        one that the table does not cover gets a slot past the cache, which a write reports and drops."""
         if page_table.dim() != 2 or page_table.shape[1] < 1:
             raise ValueError("page_table: expected [B, width], width at least 1")
         if positions.shape != page_table.shape[:1]:
@@ -683,7 +683,7 @@ class KVCache:
         page = torch.gather(page_table.long(), 1, column.clamp(max=page_table.shape[1] - 1)[:, None])[:, 0]
         slot = page * self.page_size + at % self.page_size
         past = self.k.shape[0] * self.page_size
-        slot = torch.where((column >= page_table.shape[1]) | (page < 0), past, slot)
+        slot = torch.where(column >= page_table.shape[1], past, slot)
         return torch.where(pos < 0, -1, slot)
 
     def nbytes(self) -> int:

@@ -87,6 +87,25 @@ def test_rows_of_zeros_infinities_and_nan():
     assert np.isfinite(qs[good]).all()
 
 
+@pytest.mark.parametrize("wsize,xsize", [(1e-35, 1e-3), (5e-36, 1e-4), (1e-34, 1e-3), (1e30, 1e-3)])
+def test_weights_at_the_ends_of_the_range(wsize, xsize):
+    """Products h w so small that 127 / max|h w| is no float32 number, or subnormal themselves, under a scale
+    that is a normal one; and large ones.  A subnormal product is off by 2^-150, which is 2^-21 of a largest
+    one of at least 2^-129."""
+    x, res, w = case(5, 512, 3)
+    x, res = (bf16.from_f64(xsize * bf16.to_f64(t)) for t in (x, res))
+    w = bf16.from_f64(wsize * bf16.to_f64(w))
+    q, qs, h = api.w4_rms_add_q8(dev(x), dev(res), dev(w))
+    _, y_ref = decode.rms_add(x, res, w, api.RMS_EPS)
+    s_ref = np.abs(y_ref).max(axis=1) / 127
+    assert (s_ref > 2.0 ** -126).all() and (np.abs(host_f64(h) * bf16.to_f64(w)).max(axis=1) > 2.0 ** -129).all()
+    s = qs.cpu().numpy().astype(np.float64)
+    slack = chain(512) + 2.0 ** -21
+    assert (np.abs(s - s_ref) <= s_ref * slack * 1.01).all()
+    qq = q.cpu().numpy().astype(np.float64)
+    assert (np.abs(qq - y_ref / s_ref[:, None]) <= 0.5 + 127 * 3 * slack).all()
+
+
 def test_residual_updated_in_place_and_rows_beside_left_alone():
     x, res, w = case(33, 2816, 9)
     want_y, want_h = api.w4_rms_add(dev(x), dev(res), dev(w))

@@ -118,8 +118,8 @@ rms_add_kernel(const uint16_t* __restrict__ x, const uint16_t* residual, const u
       for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(fmaf(v[j], up, 12582912.f));
       uint2 o = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                            __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
-      if (!(finite && s >= 0x1p-126f)) {
-        // no scale to speak of, or a subnormal one, which need not be close to max / 127
+      if (!(finite && s >= 0x1p-126f && __uint_as_float(amax) >= 0x1p-120f)) {
+        // no scale to speak of; a subnormal one, which need not be close to max / 127; or 127 / max past float32
         o = make_uint2(0, 0);
         if (finite && s > 0.f) {
           uint32_t b[2] = {0, 0};

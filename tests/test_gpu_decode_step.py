@@ -178,3 +178,66 @@ def test_step_on_another_stream():
     got = st.decode_step(x0, logits, blocks, table, lens, slots, stream=other)[0]
     other.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+def test_padded_rows_leave_the_others_alone(kind):
+    """Rows of length 0 without a slot: whatever they hold, the others' results and the caches stay the same."""
+    outs = []
+    for other in range(2):
+        st, blocks, table, r = build(kind, seed=6)
+        x0, logits = inputs(r, 5)
+        lens = torch.tensor([1, 0, 1, 0, 1], dtype=torch.int32, device="cuda")
+        for step in range(3):
+            if other:
+                x0[[1, 3]] = 100 * torch.randn((2, H), device="cuda").to(torch.bfloat16)
+            slots = blocks[0].cache.slots(table, lens - 1)
+            assert (slots[[1, 3]] == -1).all()
+            n, h = st.decode_step(x0, logits, blocks, table, lens, slots)
+            lens += (lens > 0).int()
+        outs.append((n[::2], h[::2], [b.cache.k for b in blocks], [b.cache.v for b in blocks]))
+    a, b = outs
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for i in (2, 3):
+        assert all(torch.equal(p, q) for p, q in zip(a[i], b[i]))
+
+
+def test_two_captured_blocks_replayed_side_by_side():
+    """Attention blocks captured one after the other share no scratch: replayed at once they give the eager bits."""
+    sides = []
+    for seed in (7, 8):
+        _, blocks, table, r = build("int8", seed=seed)
+        x, h = (dev_bf16(bf16.from_f64(r.randn(5, H))) for _ in range(2))
+        lens = torch.full((5,), 40, dtype=torch.int32, device="cuda")
+        slots = blocks[0].cache.slots(table, lens - 1)
+        want = [t.clone() for t in blocks[0](x, h, table, lens, slots)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = blocks[0](x, h, table, lens, slots)
+        # a graph reads its inputs where they were: they are kept with it
+        sides.append((g, got, want, torch.cuda.Stream(), (blocks, x, h, table, lens, slots)))
+    for _ in range(30):
+        for g, _, _, stream, _ in sides:
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, got, want, *_ in sides:
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_a_step_on_another_stream_keeps_its_tensors_there():
+    """A step given a stream allocates on it: tensors that it drops are not handed to the current stream
+    while its kernels still use them."""
+    st, blocks, table, r = build("int8", seed=4)
+    x0, logits = inputs(r, 5)
+    lens = torch.ones(5, dtype=torch.int32, device="cuda")
+    slots = blocks[0].cache.slots(table, lens - 1)
+    want = st.decode_step(x0, logits, blocks, table, lens, slots)[0].clone()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(10):
+        got = st.decode_step(x0, logits, blocks, table, lens, slots, stream=other)[0]
+        spoil = [torch.full((5, H), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert len(spoil) == 8 and torch.equal(got, want)

@@ -459,6 +459,13 @@ def _scratch(ws, nbytes: int, dev):
     return ws.data_ptr(), ws.numel(), ws
 
 
+def linear_scratch(M: int, N: int, words: int, dev) -> torch.Tensor | None:
+    """Scratch for one w4a16_linear call on codes [N, words] from torch's stream-ordered allocator (None when it
+    needs none): unlike workspace()'s buffers, two captured graphs never share it."""
+    n = _bytes_needed(_lib.W4_OP_LINEAR, M, N, 8 * words, 1, dev.index)
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
 def _rms_args(x, residual, weight, h):
     if x.dtype is not torch.bfloat16 or not x.is_contiguous():
         _need("x", x, torch.bfloat16)

@@ -31,6 +31,11 @@ class RepackReport:
     group_m_down: torch.Tensor        # uint8 [L*E*H, I/32]
 
 
+def _placed(x, stream):
+    """Context in which calls without a stream run on `stream`, or on the current stream of x's device."""
+    return torch.cuda.device(x.device) if stream is None else torch.cuda.stream(stream)
+
+
 class AttentionBlock:
     """The attention half of a decoder layer on 4-bit weights, for one new token per sequence:
 
@@ -58,14 +63,15 @@ class AttentionBlock:
         """x bf16 [T, H] (the previous layer's output), h bf16 [T, H] the residual stream or None for
         the first layer; page_table, seq_lens as in kv_cache_attend (the new token counted), slots
         int64 [T] of the new rows -> (the expert layer's input, h)."""
-        T = x.shape[0]
-        n, ns, h = api.w4_rms_add_q8(x, h, self.norm_in, stream=stream)
-        rows = api.w4a8_linear(n, ns, *self.qkv, stream=stream).unflatten(1, (-1, self.dim))
-        q, k, v = rows.split((self.q_heads, self.kv_heads, self.kv_heads), dim=1)
-        self.cache.write(k, v, slots, stream=stream)
-        a = self.cache.attend(q, page_table, seq_lens, softcap=self.softcap, window=self.window, stream=stream)
-        o = api.w4a16_linear(a.view(T, -1), *self.o, stream=stream)
-        return api.w4_rms_add(o, h, self.norm_out, stream=stream)
+        with _placed(x, stream):
+            T = x.shape[0]
+            n, ns, h = api.w4_rms_add_q8(x, h, self.norm_in)
+            rows = api.w4a8_linear(n, ns, *self.qkv).unflatten(1, (-1, self.dim))
+            q, k, v = rows.split((self.q_heads, self.kv_heads, self.kv_heads), dim=1)
+            self.cache.write(k, v, slots)
+            a = self.cache.attend(q, page_table, seq_lens, softcap=self.softcap, window=self.window)
+            o = api.w4a16_linear(a.view(T, -1), *self.o, ws=api.linear_scratch(T, *self.o[0].shape, x.device))
+            return api.w4_rms_add(o, h, self.norm_out)
 
 
 class MoEStack:
@@ -148,15 +154,18 @@ class MoEStack:
         """One decode step through attention and experts: layer l runs blocks[l] (AttentionBlock, each
         with its own cache; they share page_table, seq_lens and slots) and expert layer l on
         logits[l] f32 [T, E], around the residual stream that x0 bf16 [T, H] begins.  Returns
-        (norm of the final residual stream with weight `norm`, the stream), both bf16 [T, H]."""
+        (norm of the final residual stream with weight `norm`, the stream), both bf16 [T, H].  Rows whose
+        slot is negative and whose length is 0 are padding.  The expert layers share scratch and keep their
+        buffers: two steps must not overlap on the GPU, nor two captured ones be replayed at once."""
         if len(blocks) != self.L:
             raise ValueError(f"blocks: expected {self.L}, got {len(blocks)}")
         T = x0.shape[0]
-        y, h = x0, None
-        for l, block in enumerate(blocks):
-            x, h = block(y, h, page_table, seq_lens, slots, stream=stream)
-            y = self.layer(l, T, fused)(x, logits[l], stream=stream)
-        return api.w4_rms_add(y, h, norm, stream=stream)
+        with _placed(x0, stream):
+            y, h = x0, None
+            for l, block in enumerate(blocks):
+                x, h = block(y, h, page_table, seq_lens, slots)
+                y = self.layer(l, T, fused)(x, logits[l])
+            return api.w4_rms_add(y, h, norm)
 
     def expert_bytes(self) -> int:
         """Packed bytes of one expert (gate/up + down codes and scales)."""

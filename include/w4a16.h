@@ -329,7 +329,7 @@ w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint1
  *   M >= 0, N >= 1, K >= 32 with K % 32 == 0.
  *   workspace at least w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1) bytes (may be NULL when that
  *             is 0).  Its contents need no preparation; calls sharing it must not overlap on the GPU.
- * Up to 64 rows, and for shapes that the tensor-memory kernel of w4a16_linear does not take, sums
+ * Up to 32 rows, and for shapes that the tensor-memory kernel of w4a16_linear does not take, sums
  * inside a group are exact integers and groups are accumulated in float32 in a fixed order.  More rows
  * of shapes that it takes (N % 128 == 0, K % 64 == 0, K <= 4096, scales 4-byte aligned) go to that kernel
  * where it is the faster one: every product is exact, the sums are float32.  Either way a call gives the

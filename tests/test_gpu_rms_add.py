@@ -164,7 +164,9 @@ def test_linear_wider(M, N, K):
     check_linear(*linear_case(M, N, K, 11))
 
 
-@pytest.mark.parametrize("M,N,K,off", [(900, 5632, 1024, 0), (1025, 3584, 1088, 0), (900, 5632, 1024, 1)])
+@pytest.mark.parametrize("M,N,K,off", [(900, 5632, 1024, 0), (1025, 3584, 1088, 0), (900, 5632, 1024, 1),
+                                       (509, 8192, 448, 0), (300, 16384, 832, 0), (64, 14336, 4096, 0), (64, 14336, 4096, 1),
+                                       (385, 9472, 64 * 17, 0), (257, 9472, 2048, 0)])
 def test_linear_many_rows(M, N, K, off):
     xq, xs, codes, scales = linear_case(M, N, K, 5)
     xs[7] = np.nan

@@ -172,53 +172,54 @@ a_to_f16_short_kernel(const uint16_t* __restrict__ a, const int32_t* __restrict_
 }
 
 // 8-bit activation rows to the same fp16 layout, exactly (|x| <= 128), and the weight rows' exponents of
-// row_exp_kernel, in one launch: a warp per row of either.  The rows' scales are the row multipliers, copied.
+// row_exp_kernel, in one launch: x_blocks blocks take 16 elements a thread, wherever a row begins, the others 8
+// lanes a weight row.  The rows' scales are the row multipliers, copied.  K <= 4096 (K / 64 words of scales a row).
+// Nothing is behind anything else: 8192 x 2816 weights and 509 rows took 5.6 us with a warp a row of either.
+constexpr int kScaleWords = 4096 / 64 / 8;                 // of a lane
 __global__ void __launch_bounds__(256)
-a8_to_f16_kernel(const int8_t* __restrict__ x, const float* __restrict__ xs, int64_t rows, int K,
+a8_to_f16_kernel(const int8_t* __restrict__ x, const float* __restrict__ xs, int64_t rows, int K, int x_blocks,
                  uint16_t* __restrict__ a16, float* __restrict__ rowmul, const uint16_t* __restrict__ scales,
                  int64_t wrows, int8_t* __restrict__ e_out) {
-  const int lane = threadIdx.x & 31;
-  const int64_t first = blockIdx.x * 8LL + (threadIdx.x >> 5), step = gridDim.x * 8LL;
-  for (int64_t i = first; i < rows + wrows; i += step) {
-    if (i < rows) {
-      const uint2* src = reinterpret_cast<const uint2*>(x + i * K);
-      uint4* dst = reinterpret_cast<uint4*>(a16 + i * K);
-      for (int c0 = 0; c0 < K / 8; c0 += 128) {
-        uint2 v[4];
+  pdl_trigger();                                           // (the GEMM waits where it reads these results)
+  if (static_cast<int>(blockIdx.x) < x_blocks) {
+    const int64_t i = blockIdx.x * 256LL + threadIdx.x;
+    if (i < rows) rowmul[i] = __ldg(xs + i);               // (fewer rows than threads: K >= 16)
+    if (i >= rows * (K / 16)) return;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + 32 * j + lane;
-          v[j] = c < K / 8 ? __ldg(src + c) : make_uint2(0, 0);
-        }
+    for (int h = 0; h < 2; ++h) {
+      // elements (p, p + 4) of 8, offset by 128 in the low mantissa of 1024, less 1152
+      const uint32_t u0 = w[2 * h] ^ 0x80808080u, u1 = w[2 * h + 1] ^ 0x80808080u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + 32 * j + lane;
-          if (c >= K / 8) continue;
-          // elements (p, p + 4) offset by 128 in the low mantissa of 1024, less 1152
-          const uint32_t u0 = v[j].x ^ 0x80808080u, u1 = v[j].y ^ 0x80808080u;
-          uint32_t o[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t b = (__byte_perm(u0, u1, p | (4 + p) << 8) & 0x00FF00FFu) | 0x64006400u;
-            const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), __half2half2(__ushort_as_half(0x6480)));
-            o[p] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t b = (__byte_perm(u0, u1, p | (4 + p) << 8) & 0x00FF00FFu) | 0x64006400u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&b), __half2half2(__ushort_as_half(0x6480)));
+        o[4 * h + p] = *reinterpret_cast<const uint32_t*>(&d);
       }
-      if (lane == 0) rowmul[i] = __ldg(xs + i);
-    } else {
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(scales + (i - rows) * (K / 32));
-      uint32_t m = 0;
-      for (int j = lane; j < K / 64; j += 32) {
-        const uint32_t v = __ldg(row + j), lo = v & 0x7FFFu, hi = (v >> 16) & 0x7FFFu;
-        if (lo < 0x7F80u) m = max(m, lo);
-        if (hi < 0x7F80u) m = max(m, hi);
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) e_out[i - rows] = static_cast<int8_t>(shift_for(m, 10));
     }
+    uint4* dst = reinterpret_cast<uint4*>(a16) + 2 * i;
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return;
   }
+  const int64_t row = (blockIdx.x - x_blocks) * 32LL + (threadIdx.x >> 3);
+  const int lane = threadIdx.x & 7, words = K / 64;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(scales + (row < wrows ? row : 0) * (K / 32));
+  uint32_t v[kScaleWords];
+#pragma unroll
+  for (int j = 0; j < kScaleWords; ++j) v[j] = 8 * j + lane < words ? __ldg(src + 8 * j + lane) : 0u;
+  uint32_t m = 0;                                          // the largest finite |scale|
+#pragma unroll
+  for (int j = 0; j < kScaleWords; ++j) {
+    const uint32_t lo = v[j] & 0x7FFFu, hi = (v[j] >> 16) & 0x7FFFu;
+    if (lo < 0x7F80u) m = max(m, lo);
+    if (hi < 0x7F80u) m = max(m, hi);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0 && row < wrows) e_out[row] = static_cast<int8_t>(shift_for(m, 10));
 }
 
 }  // namespace cv
@@ -278,9 +279,9 @@ void w4_launch_a_to_f16(const uint16_t* a, const int32_t* a_row_of_pair, int k_d
 }
 
 void w4_launch_a8_to_f16(const int8_t* x, const float* xs, int64_t rows, int K, const uint16_t* scales, int64_t wrows,
-                         void* ws, cudaStream_t stream, int sm_count) {
-  const int64_t blocks = (rows + wrows + 7) / 8;
-  const int grid = static_cast<int>(blocks < 8LL * sm_count ? blocks : 8LL * sm_count);
-  w4::cv::a8_to_f16_kernel<<<grid, 256, 0, stream>>>(x, xs, rows, K, w4_ws_a16(ws), w4_ws_rowmul(ws, rows, K), scales,
-                                                     wrows, w4_ws_rowexp(ws, rows, K));
+                         void* ws, cudaStream_t stream) {
+  const int64_t x_blocks = (rows * (K / 16) + 255) / 256, blocks = x_blocks + (wrows + 31) / 32;
+  w4::cv::a8_to_f16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+      x, xs, rows, K, static_cast<int>(x_blocks), w4_ws_a16(ws), w4_ws_rowmul(ws, rows, K), scales, wrows,
+      w4_ws_rowexp(ws, rows, K));
 }

@@ -144,7 +144,7 @@ void w4_launch_a_to_f16(const uint16_t* a, const int32_t* a_row_of_pair, int k_d
                         int32_t* dev_status, cudaStream_t stream, int sm_count);
 // The same from 8-bit rows with one scale each: exact fp16 values, the scales as row multipliers.
 void w4_launch_a8_to_f16(const int8_t* x, const float* xs, int64_t rows, int K, const uint16_t* scales, int64_t wrows,
-                         void* ws, cudaStream_t stream, int sm_count);
+                         void* ws, cudaStream_t stream);
 // pointers into a workspace laid out by w4_tc_workspace_bytes
 uint16_t* w4_ws_a16(void* ws);
 float* w4_ws_rowmul(void* ws, int64_t rows, int K);

@@ -106,7 +106,12 @@ struct Cfg {
   static constexpr int kCodePitch = KSK / 2;             // bytes of one code row in a stage
   static constexpr int kCodeStage = kBM * kCodePitch;
   static constexpr int kTokSub = NMAX * 128;             // one 64-k sub-tile: NMAX rows x 128 B
-  static constexpr int kTokStage = kSubs * kTokSub;
+  // 64-k sub-tiles a token slot holds: a stage's, or one where a stage's are 64 KB (256 rows), so that five slots fit
+  // in place of two (2048 x 8192 x 4096 dense 8-bit rows 121 us, 123 with two).
+  static constexpr int kRingSubs = NMAX > 192 ? 1 : kSubs;
+  static constexpr int kRingParts = kSubs / kRingSubs;   // slots a stage
+  static constexpr int kTokStage = kRingSubs * kTokSub;  // bytes of a slot
+  static_assert(kRingParts == 1 || (KSK == 128 && KSPLIT == 1), "slots of one sub-tile: one TMEM slot a stage, one k part");
   static_assert(ABUF == 1 || ABUF == 2, "accumulator buffers");
   static_assert(EPIW == 1 || EPIW == 2, "epilogue warps per TMEM lane quadrant");
   static constexpr int kIssuers = NSPLIT * KSPLIT;
@@ -342,6 +347,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
     // ---------------------------- token producer ----------------------------
     if (lane == 0) {
       prefetch_tmap(&tmap_tok);
+      pdl_wait();                              // the converted rows
       int slot = 0;
       uint32_t ph = 0;
       bool lap0 = true, ok = true;
@@ -350,13 +356,13 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
         Tile T;
         decode_tile(A, table, offs, t, NMAX, T);
         const int32_t r0 = static_cast<int32_t>(T.r0);
-        for (int st = 0; st < nst; ++st) {
+        for (int st = 0; st < nst * C::kRingParts; ++st) {
           if (!lap0 && !mbar_wait(&tfree[slot], ph)) { ok = false; break; }
           uint8_t* tdst = smem + C::tok + slot * C::kTokStage;
           mbar_arrive_expect_tx(&tfull[slot], C::kTokStage);
 #pragma unroll
-          for (int sub = 0; sub < C::kSubs; ++sub)
-            tma_load_2d(tdst + sub * C::kTokSub, &tmap_tok, st * KSK + 64 * sub, r0, &tfull[slot]);
+          for (int sub = 0; sub < C::kRingSubs; ++sub)
+            tma_load_2d(tdst + sub * C::kTokSub, &tmap_tok, (st * C::kRingSubs + sub) * 64, r0, &tfull[slot]);
           ++issued;
           if (++slot == TSTAGES) { slot = 0; if (!lap0) ph ^= 1u; lap0 = false; }
         }
@@ -392,6 +398,29 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
         const uint32_t d_tmem = tmem_base + C::acc_col(ab, ksi) + nsi * C::kNS;
         bool first = true;
         for (int st = 0; st < nst && ok; ++st) {
+          if constexpr (C::kRingParts > 1) {
+            // one TMEM slot, token slots of 64 k: each is released as soon as its MMAs have read it
+            if (!mbar_wait(&a_ready[aslot], aph)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_tm = tmem_base + C::kA0 + aslot * kACols;
+            for (int part = 0; part < C::kRingParts; ++part) {
+              if (!mbar_wait(&tfull[slot], ph)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t tb = smem_u32(smem + C::tok + slot * C::kTokStage) + nsi * C::kNS * 128;
+              if (n_my > 0 && st * KSK + part * 64 < A.K) {         // (K % 64 == 0)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  mma_f16_ts(d_tmem, a_tm + 8 * (4 * part + j), sw128_desc(tb + j * 32), idesc, first ? 0u : 1u);
+                  first = false;
+                }
+              }
+              mma_commit(&tfree[slot]);
+              if (++slot == TSTAGES) { slot = 0; ph ^= 1u; }
+            }
+            mma_commit(&a_free[aslot]);
+            if (++aslot == ASLOTS) { aslot = 0; aph ^= 1u; }
+            continue;
+          }
           if (!mbar_wait(&tfull[slot], ph)) { ok = false; break; }
           const uint32_t tb = smem_u32(smem + C::tok + slot * C::kTokStage) + nsi * C::kNS * 128;
           for (int hf = 0; hf < C::kHalves; ++hf) {
@@ -437,6 +466,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
     uint8_t* stg = smem + L.stage + (q + 4 * cp) * 2048;
     int n_out = 0;                                 // TMA stores issued by this warp (lane 0)
     int ti = 0;
+    pdl_wait();                                    // the row multipliers
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       Tile T;
       decode_tile(A, table, offs, t, NMAX, T);
@@ -581,6 +611,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
 #pragma unroll
     for (int i = 0; i < kSQ; ++i) sq[i] = pf_next();
     // exponent of this row, one tile ahead
+    pdl_wait();
     int e_next = 0;
     if (blockIdx.x < static_cast<unsigned>(total)) {
       Tile T0;
@@ -716,7 +747,7 @@ static bool tm_layout(int E, int kg, w4::tm::Lay& L) {
 
 template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW>
 static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64_t rows, int K,
-                               w4::tm::Args A, cudaStream_t stream, int sm_count) {
+                               w4::tm::Args A, cudaStream_t stream, int sm_count, bool early) {
   using C = w4::tm::Cfg<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>;
   auto fn = tm_encode_fn();
   if (!fn) return W4_ERR_CUDA;
@@ -776,14 +807,17 @@ static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64
       return W4_ERR_CUDA;
     attr_done[dev] = 1;
   }
-  w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>
-      <<<sm_count, 32 * C::kWarps, smem, stream>>>(tmap_codes, tmap_tok, tmap_out, A);
+  auto kernel = w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>;
+  if (early)
+    return launch_pdl(kernel, dim3(sm_count), dim3(32 * C::kWarps), smem, stream, tmap_codes, tmap_tok, tmap_out,
+                          A) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+  kernel<<<sm_count, 32 * C::kWarps, smem, stream>>>(tmap_codes, tmap_tok, tmap_out, A);
   return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count);
+                                cudaStream_t stream, int sm_count, int block, bool early);
 
 w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int k_div,
                             const uint32_t* codes, const uint16_t* scales, const int32_t* offsets,
@@ -802,13 +836,14 @@ w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int
   w4_launch_a_to_f16(a, a_row_of_pair, kd, a_rows, rows, K, scales, wrows, ws, dev_status, stream,
                      sm_count);
 
-  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count);
+  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count, 192, false);
 }
 
-// The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16).
+// The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16), in
+// blocks of 192 or 256 rows.  early: the conversion kernel lets this one begin while it runs (w4_launch_a8_to_f16).
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count) {
+                                cudaStream_t stream, int sm_count, int block, bool early) {
   w4::tm::Args A{};
   A.rowmul = w4_ws_rowmul(ws, rows, K);
   A.rowexp = w4_ws_rowexp(ws, rows, K);
@@ -818,9 +853,10 @@ w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, c
   A.n_tiles = (epi == W4_EPI_GELU_GATE) ? (N / 2) / (w4::tm::kBM / 2) : N / w4::tm::kBM;
   A.dev_status = dev_status;
   const uint16_t* a16 = w4_ws_a16(ws);
+  if (block == 256) return tm_launch_cfg<256, 128, 5, 4, 1, 1, 1, 2>(codes, a16, rows, K, A, stream, sm_count, early);
   // 192-row token blocks, 128-k stages with three token stages in flight, one MMA-issuing thread
   // (N = 192: every tcgen05.mma costs a fixed time on top of its columns, so fewer, wider MMAs
   // finish sooner than two threads' 96-column ones), two 192-column accumulators drained by eight
   // epilogue warps
-  return tm_launch_cfg<192, 128, 3, 2, 1, 1, 2, 2>(codes, a16, rows, K, A, stream, sm_count);
+  return tm_launch_cfg<192, 128, 3, 2, 1, 1, 2, 2>(codes, a16, rows, K, A, stream, sm_count, early);
 }

@@ -14,7 +14,8 @@
 // each warp streams through its own ring of stages (TMA tiles) with no block-wide wait; the rows lie in
 // shared memory as ready operands.  More rows: tiles of 128 weight rows by 16 to 64 tokens, 256 k a stage.
 // Many rows of shapes that fit it: the tensor-memory kernel of tm_gemm.cu on fp16 rows, to which 8-bit rows
-// convert exactly; there a sum runs over products of 24 bits, exact each, in float32 throughout.
+// convert exactly; there a sum runs over products of 24 bits, exact each, in float32 throughout.  It begins on the
+// codes while the conversion runs (512 x 2816 x 2816 24.0 us, 25.4 one after the other).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -25,7 +26,7 @@
 bool w4_tm_supported(int N, int K, int epi);
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count);
+                                cudaStream_t stream, int sm_count, int block, bool early);
 
 namespace w4 {
 namespace a8 {
@@ -516,24 +517,30 @@ int64_t many_tiles(int64_t M, int64_t N) {
   return (M + BM - 1) / BM * ((N + kBN - 1) / kBN);
 }
 
-// Whether the tensor-memory kernel is the faster one for shapes that it takes.  It works in tiles of 128 weight
-// rows by 192 tokens, one an SM at a time, about K * 9 ns each (37 us at K 4096), behind a conversion of about
-// 5 us; the kernel above runs two tiles of 128 by 64 an SM in about K * 11 ns, and can split K where there are
-// fewer tiles than SMs.  Measured, that one first: 509 x 8192 x 2816 67 us and 42; 2048 x 8192 x 4096 308 and
-// 128; 512 x 2816 x 2816 36 and 26; 128 x 14336 x 4096 49 and 35; 64 x 14336 x 4096 35 (stays).
-bool use_tm(int64_t M, int64_t N, int64_t K, int sms) {
-  const double tiles = static_cast<double>(many_tiles(M, N)), tm_tiles = static_cast<double>(N / 128) * ((M + 191) / 192);
-  if (tiles <= sms || !w4_tm_supported(static_cast<int>(N), static_cast<int>(K), W4_EPI_NONE)) return false;
-  const double tm = (tm_tiles > sms ? tm_tiles / sms : 1.0) * K * 9e-9 + 5e-6;
-  const double many = (tiles > 2 * sms ? tiles / (2 * sms) : 1.0) * K * 11e-9 + 4e-6;
-  return tm < many;
-}
-
 // Parts of K: enough to give every SM two blocks, each at least 1024 k long
 int many_splits(int64_t M, int64_t N, int64_t KG, int sms) {
   const int64_t want = 2 * sms / many_tiles(M, N), most = KG / 32;
   const int64_t s = want < most ? want : most;
   return s < 2 ? 1 : s > 16 ? 16 : static_cast<int>(s);
+}
+
+// The tensor-memory kernel's token block (0: the kernel above is the faster one, or the only one).  That one works
+// in tiles of 128 weight rows by `block` tokens, one an SM at a time, at about 5.4 ns a k of a tile for blocks of
+// 192 and 6.6 for 256, behind 7.5 us for the conversion, the beginning and the end.  Measured with 192 and 256: 509 x
+// 8192 x 2816 39.5 and 27.3 us (192 tiles or 128, for 148 SMs), 2048 x 8192 x 4096 125 and 119, 512 x 2816 x 2816
+// 23.3 and 25.4, 128 x 14336 x 4096 30.4 and 32.5.  The kernel above takes about 7.6 ns a k of a tile of 128 by 64
+// where an SM has one, 11 where it has two, on 4 us, and for a split K 2 us and the parts' bytes more: 64 x 14336 x
+// 4096 34 us (29 with the other), 33 x 28672 x 4096 49 (52), 64 x 4096 x 4096 13 (27).
+int tm_block(int64_t M, int64_t N, int64_t K, int sms) {
+  if (M > 0x7FFFFFFF - 256 || !w4_tm_supported(static_cast<int>(N), static_cast<int>(K), W4_EPI_NONE)) return 0;
+  auto waves = [&](int64_t tiles, int64_t at_once) { return static_cast<double>((tiles + at_once - 1) / at_once); };
+  const double w192 = waves(N / 128 * ((M + 191) / 192), sms) * 5.4e-9, w256 = waves(N / 128 * ((M + 255) / 256), sms) * 6.6e-9;
+  const double tm = 7.5e-6 + K * (w192 < w256 ? w192 : w256);
+  const int splits = many_splits(M, N, K / 32, sms);
+  const int64_t blocks = many_tiles(M, N) * splits;
+  double many = 4e-6 + (blocks <= sms ? 7.6e-9 : waves(blocks, 2 * sms) * 11e-9) * K / splits;
+  if (splits > 1) many += 2e-6 + splits * M * N * 8 / 6.5e12;
+  return many <= tm ? 0 : w192 < w256 ? 192 : 256;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -618,10 +625,12 @@ w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s
 size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 32 || K % 32 || N > (1LL << 30) || K > (1LL << 30)) return 0;
   if (w4::a8::few_plan(M, K / 32).S) return 0;
-  // (scales at an odd address keep the call from the tensor-memory kernel: room for either)
-  if (w4::a8::use_tm(M, N, K, w4::device_sm_count())) return w4_tc_workspace_bytes(M, static_cast<int>(K), N);
   const int splits = w4::a8::many_splits(M, N, K / 32, w4::device_sm_count());
-  return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+  const size_t parts = splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+  if (!w4::a8::tm_block(M, N, K, w4::device_sm_count())) return parts;
+  // (scales at an odd address keep the call from the tensor-memory kernel: room for either)
+  const size_t rows = w4_tc_workspace_bytes(M, static_cast<int>(K), N);
+  return rows > parts ? rows : parts;
 }
 
 extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
@@ -648,11 +657,11 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   const a8::Few f = a8::few_plan(M, K / 32);
   if (f.S)
     return w4_record_status(f.W == 16 ? a8::launch_few<16>(a, f, SB, sms, s) : a8::launch_few<8>(a, f, SB, sms, s));
-  if (a8::use_tm(M, N, K, sms) && aligned_to(scales, 4)) {
-    w4_launch_a8_to_f16(xq, xs, M, static_cast<int>(K), scales, N, workspace, s, sms);
+  if (const int block = a8::tm_block(M, N, K, sms); block && aligned_to(scales, 4)) {
+    w4_launch_a8_to_f16(xq, xs, M, static_cast<int>(K), scales, N, workspace, s);
     if (cudaGetLastError() != cudaSuccess) return w4_record_status(W4_ERR_CUDA);
     return w4_record_status(w4_launch_tm_prepared(codes, scales, nullptr, 1, M, static_cast<int>(N), static_cast<int>(K),
-                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms));
+                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms, block, true));
   }
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);

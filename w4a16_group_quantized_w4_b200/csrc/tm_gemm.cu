@@ -214,7 +214,8 @@ __device__ __forceinline__ void scale_pair(uint32_t s16, float smul, uint32_t& s
 }
 
 
-template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW>
+// EARLY: launched so that it may begin while the conversion runs; it waits where it reads the results.
+template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW, bool EARLY>
 __global__ void __launch_bounds__(32 * (16 + (NSPLIT * KSPLIT - 1) + 4 * (EPIW - 1)), 1)
 tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
                const __grid_constant__ CUtensorMap tmap_tok,
@@ -347,7 +348,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
     // ---------------------------- token producer ----------------------------
     if (lane == 0) {
       prefetch_tmap(&tmap_tok);
-      pdl_wait();                              // the converted rows
+      if constexpr (EARLY) pdl_wait();         // the converted rows
       int slot = 0;
       uint32_t ph = 0;
       bool lap0 = true, ok = true;
@@ -466,7 +467,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
     uint8_t* stg = smem + L.stage + (q + 4 * cp) * 2048;
     int n_out = 0;                                 // TMA stores issued by this warp (lane 0)
     int ti = 0;
-    pdl_wait();                                    // the row multipliers
+    if constexpr (EARLY) pdl_wait();               // the row multipliers
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       Tile T;
       decode_tile(A, table, offs, t, NMAX, T);
@@ -611,7 +612,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
 #pragma unroll
     for (int i = 0; i < kSQ; ++i) sq[i] = pf_next();
     // exponent of this row, one tile ahead
-    pdl_wait();
+    if constexpr (EARLY) pdl_wait();
     int e_next = 0;
     if (blockIdx.x < static_cast<unsigned>(total)) {
       Tile T0;
@@ -745,9 +746,9 @@ static bool tm_layout(int E, int kg, w4::tm::Lay& L) {
   return L.total <= kTmSmemBudget;
 }
 
-template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW>
+template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW, bool EARLY>
 static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64_t rows, int K,
-                               w4::tm::Args A, cudaStream_t stream, int sm_count, bool early) {
+                               w4::tm::Args A, cudaStream_t stream, int sm_count) {
   using C = w4::tm::Cfg<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>;
   auto fn = tm_encode_fn();
   if (!fn) return W4_ERR_CUDA;
@@ -802,13 +803,13 @@ static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>,
+    if (cudaFuncSetAttribute(w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW, EARLY>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess)
       return W4_ERR_CUDA;
     attr_done[dev] = 1;
   }
-  auto kernel = w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW>;
-  if (early)
+  auto kernel = w4::tm::tm_gemm_kernel<NMAX, KSK, TSTAGES, ASLOTS, NSPLIT, KSPLIT, ABUF, EPIW, EARLY>;
+  if (EARLY)
     return launch_pdl(kernel, dim3(sm_count), dim3(32 * C::kWarps), smem, stream, tmap_codes, tmap_tok, tmap_out,
                           A) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
   kernel<<<sm_count, 32 * C::kWarps, smem, stream>>>(tmap_codes, tmap_tok, tmap_out, A);
@@ -817,7 +818,7 @@ static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64
 
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int block, bool early);
+                                cudaStream_t stream, int sm_count, int early_block);
 
 w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int k_div,
                             const uint32_t* codes, const uint16_t* scales, const int32_t* offsets,
@@ -836,14 +837,15 @@ w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int
   w4_launch_a_to_f16(a, a_row_of_pair, kd, a_rows, rows, K, scales, wrows, ws, dev_status, stream,
                      sm_count);
 
-  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count, 192, false);
+  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count, 0);
 }
 
-// The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16), in
-// blocks of 192 or 256 rows.  early: the conversion kernel lets this one begin while it runs (w4_launch_a8_to_f16).
+// The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16).
+// early_block: 192 or 256, the rows of a token block after w4_launch_a8_to_f16, whose kernel lets this one begin
+// while it runs; 0 after the other.
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int block, bool early) {
+                                cudaStream_t stream, int sm_count, int early_block) {
   w4::tm::Args A{};
   A.rowmul = w4_ws_rowmul(ws, rows, K);
   A.rowexp = w4_ws_rowexp(ws, rows, K);
@@ -853,10 +855,13 @@ w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, c
   A.n_tiles = (epi == W4_EPI_GELU_GATE) ? (N / 2) / (w4::tm::kBM / 2) : N / w4::tm::kBM;
   A.dev_status = dev_status;
   const uint16_t* a16 = w4_ws_a16(ws);
-  if (block == 256) return tm_launch_cfg<256, 128, 5, 4, 1, 1, 1, 2>(codes, a16, rows, K, A, stream, sm_count, early);
+  if (early_block == 256)
+    return tm_launch_cfg<256, 128, 5, 4, 1, 1, 1, 2, true>(codes, a16, rows, K, A, stream, sm_count);
+  if (early_block == 192)
+    return tm_launch_cfg<192, 128, 3, 2, 1, 1, 2, 2, true>(codes, a16, rows, K, A, stream, sm_count);
   // 192-row token blocks, 128-k stages with three token stages in flight, one MMA-issuing thread
   // (N = 192: every tcgen05.mma costs a fixed time on top of its columns, so fewer, wider MMAs
   // finish sooner than two threads' 96-column ones), two 192-column accumulators drained by eight
   // epilogue warps
-  return tm_launch_cfg<192, 128, 3, 2, 1, 1, 2, 2>(codes, a16, rows, K, A, stream, sm_count, early);
+  return tm_launch_cfg<192, 128, 3, 2, 1, 1, 2, 2, false>(codes, a16, rows, K, A, stream, sm_count);
 }

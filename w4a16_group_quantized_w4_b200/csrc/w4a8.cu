@@ -26,7 +26,7 @@
 bool w4_tm_supported(int N, int K, int epi);
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int block, bool early);
+                                cudaStream_t stream, int sm_count, int early_block);
 
 namespace w4 {
 namespace a8 {
@@ -661,7 +661,7 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
     w4_launch_a8_to_f16(xq, xs, M, static_cast<int>(K), scales, N, workspace, s);
     if (cudaGetLastError() != cudaSuccess) return w4_record_status(W4_ERR_CUDA);
     return w4_record_status(w4_launch_tm_prepared(codes, scales, nullptr, 1, M, static_cast<int>(N), static_cast<int>(K),
-                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms, block, true));
+                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms, block));
   }
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);

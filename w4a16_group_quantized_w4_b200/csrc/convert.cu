@@ -37,7 +37,7 @@ a_to_f16_kernel(const uint16_t* __restrict__ a, const int32_t* __restrict__ a_ro
     }
     const uint4* src = reinterpret_cast<const uint4*>(a + srow * K);
     // lane l holds chunks l, l + 32, ... of up to kCB * 32 chunks at a time, all loads in
-    // flight together; a row of at most kCB * 256 elements (K <= 3072) is read once
+    // flight together; a row of at most kCB * 256 elements is read once
     constexpr int kCB = 12;
     uint4 v[kCB];
     uint32_t m = 0;

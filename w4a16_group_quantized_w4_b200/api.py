@@ -397,7 +397,7 @@ def _device_call(fn):
                 raise ValueError(f"stream: expected device {dev}, got {stream.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kw)
-        if dev.index != torch.cuda.current_device():
+        if dev.index != _current_device():
             with torch.cuda.device(dev):
                 return fn(*args, **kw)
         return fn(*args, **kw)
@@ -412,6 +412,8 @@ def _cur(dev) -> int:
 
 
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# (a CUDA tensor is at hand where this is called, so CUDA is up)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _fits(name, t, dtype, shape, dev):
@@ -505,7 +507,7 @@ def w4_rms_add_q8(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, q
     """w4_rms_add with 8-bit rows: (q int8 [T, H], q_scale f32 [T], h), y = q_scale * q."""
     shape, dev, h = _rms_args(x, residual, weight, h)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8)
     else:
         _fits("q", q, torch.int8, shape, dev)
     if q_scale is None:
@@ -530,7 +532,7 @@ def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
     _fits("codes", codes, torch.int32, (N, K // 8), dev)
     _fits("scales", scales, torch.bfloat16, (N, K // 32), dev)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=dev)   # (torch.empty: 0.9 us more)
     else:
         _fits("y", y, torch.bfloat16, (M, N), dev)
     p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_LINEAR_8, M, N, K, 1, dev.index), dev)
@@ -593,11 +595,11 @@ def kv_cache_read(slots, k_cache, v_cache, k_scales=None, v_scales=None, k=None,
     _fits("slots", slots, torch.int64, (T,), dev)
     want = (T, heads, dim)
     if k is None:
-        k = torch.empty(want, dtype=torch.bfloat16, device=dev)
+        k = torch.empty_strided(want, (heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
     else:
         _fits("k", k, torch.bfloat16, want, dev)
     if v is None:
-        v = torch.empty(want, dtype=torch.bfloat16, device=dev)
+        v = torch.empty_like(k)
     else:
         _fits("v", v, torch.bfloat16, want, dev)
     if dev_status is not None:

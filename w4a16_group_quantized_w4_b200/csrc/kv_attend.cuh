@@ -96,7 +96,9 @@ inline int64_t recs_bytes(int sms) { return (static_cast<int64_t>(sms) * kMostBl
 
 // 16-token tiles a stage, stages of a warp's ring and blocks per SM, by [whole][kind][head_dim / 64 - 1]: for
 // long streams, and for items that a block takes whole (short ones: more blocks hide the way to their first
-// bytes, and deep rings would not fill).
+// bytes, and deep rings would not fill).  Swept: of int8, 128, 64 sequences to 8192 tokens, {1, 3, 3} takes 74 us,
+// {1, 2, 4} 84, {1, 3, 4} 97, {1, 4, 3} 117; of int4, 256, 48 windows of 16384, {1, 3, 3}
+// takes 58 us, {2, 2, 2} 61, {1, 4, 3} 78, {2, 3, 2} 80; bf16 wants the deepest rings that fit.
 struct Shape {
   int tiles, stages, blocks;
 };

@@ -12,7 +12,8 @@
 // beside them of the value row; two neighbouring lanes share a group, so its maximum takes one shuffle.
 // Measured for 8192 tokens of 8 heads of 128 to int8: 23.4 us with a division per element, 19.2 us with a
 // reciprocal and a Newton step, 15.1 us with packed maxima, whole-warp shuffles and divisions of indexes by
-// multiplication, 12.9 us (4.0 TB/s; 5.6 for 32768 tokens) with 16 elements a thread instead of 8.  A reading
+// multiplication, 12.4 us with 16 elements a thread instead of 8, 12.1 us (4.3 TB/s; 5.2 for 32768 tokens) with
+// quotients in pairs.  A reading
 // thread takes 8 of each, twice, so that a warp's stores fill whole lines: 32768 int8 tokens take 36 us (5.6
 // TB/s), 45 us with 16 elements a thread.
 #include "common.cuh"
@@ -76,10 +77,21 @@ __device__ __forceinline__ Chunk chunk_of(uint32_t i, const Shape& s, const int6
 
 constexpr int kThreads = 256;
 
-// rint(x / s) + bias in the low bits of a float of 1.5 * 2^23 and more; s positive and normal, inv near 1 / s
-__device__ __forceinline__ uint32_t quotient(float x, float s, float inv, float bias) {
-  const float q = x * inv;
-  return __float_as_uint(fmaf(fmaf(-q, s, x), inv, q) + (12582912.f + bias));
+// rint(x / s) + bias of two elements in the low bits of floats of 1.5 * 2^23 and more; s positive and normal, inv
+// near 1 / s.  As packed float32 pairs: the negative of s and the bias come as pairs too.
+__device__ __forceinline__ uint64_t twice(float v) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ void quotients(uint32_t x2, uint64_t minus_s, uint64_t inv, uint64_t bias, uint32_t& lo, uint32_t& hi) {
+  uint64_t x, q, e;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(bf16_lo_to_f32(x2)), "f"(bf16_hi_to_f32(x2)));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(inv));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(minus_s), "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(e), "l"(inv));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(q) : "l"(bias));
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(q));
 }
 // the low bytes of four words
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -109,11 +121,9 @@ __device__ __forceinline__ uint32_t quantise16(const uint32_t (&w)[8], uint32_t 
     // so nothing has to be clamped.
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint64_t minus_s2 = twice(-s), inv2 = twice(inv), bias2 = twice(12582912.f + kBias);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[2 * j] = quotient(bf16_lo_to_f32(w[j]), s, inv, kBias);
-      c[2 * j + 1] = quotient(bf16_hi_to_f32(w[j]), s, inv, kBias);
-    }
+    for (int j = 0; j < 8; ++j) quotients(w[j], minus_s2, inv2, bias2, c[2 * j], c[2 * j + 1]);
   } else {                                                // (a subnormal step can be far below max / top)
 #pragma unroll
     for (int j = 0; j < 16; ++j) {

@@ -250,6 +250,32 @@ __device__ __forceinline__ float tanh_fast(float y) {
   return fmaf(-2.f, r, 1.f);
 }
 
+// Float32 pairs, both elements in one instruction: (a, b) *= (c, d), += (c, d), += (c, d) f.  (Scores, weights and
+// totals in pairs: 48 int4 windows of 16384 tokens 57.8 us, singly 58.7.)
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void mul_pair(float& a, float& b, float c, float d) {
+  uint64_t v = pair_of(a, b);
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(pair_of(c, d)));
+  unpair(v, a, b);
+}
+__device__ __forceinline__ void add_pair(float& a, float& b, float c, float d) {
+  uint64_t v = pair_of(a, b);
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(pair_of(c, d)));
+  unpair(v, a, b);
+}
+__device__ __forceinline__ void fma_pair(float& a, float& b, float c, float d, float f) {
+  uint64_t v = pair_of(a, b);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(pair_of(c, d)), "l"(pair_of(f, f)));
+  unpair(v, a, b);
+}
+
 // D += A(16x8 bf16) * B(8x8 bf16)
 __device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
@@ -541,10 +567,8 @@ struct Worker {
             const uint32_t w0 = ksc[0][g / 2], w1 = ksc[1][g / 2];
             const float s0 = g & 1 ? bf16_hi_to_f32(w0) : bf16_lo_to_f32(w0);
             const float s1 = g & 1 ? bf16_hi_to_f32(w1) : bf16_lo_to_f32(w1);
-            s[e][x][0] = fmaf(c[0], s0, s[e][x][0]);
-            s[e][x][1] = fmaf(c[1], s0, s[e][x][1]);
-            s[e][x][2] = fmaf(c[2], s1, s[e][x][2]);
-            s[e][x][3] = fmaf(c[3], s1, s[e][x][3]);
+            fma_pair(s[e][x][0], s[e][x][1], c[0], c[1], s0);
+            fma_pair(s[e][x][2], s[e][x][3], c[2], c[3], s1);
           }
         }
       }
@@ -557,7 +581,7 @@ struct Worker {
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][i] *= zmul[e][i & 1];
+      for (int i = 0; i < 4; i += 2) mul_pair(s[x][i], s[x][i + 1], zmul[e][0], zmul[e][1]);
     if (a.softcap > 0.f) {
       // cap(z) = softcap tanh(z / softcap), in log2 units on both sides
       const float cap = a.softcap * 1.4426950408889634f, in = 2.f / a.softcap;
@@ -590,14 +614,19 @@ struct Worker {
         for (int i = 0; i < D / 16; ++i) { acc[e][i][c] *= f; acc[e][i][2 + c] *= f; }
       }
     }
-    const float ref[2] = {kBf ? m[e][0] : m[e][0] - kLift, kBf ? m[e][1] : m[e][1] - kLift};
+    const float less[2] = {kBf ? -m[e][0] : kLift - m[e][0], kBf ? -m[e][1] : kLift - m[e][1]};
 #pragma unroll
     for (int x = 0; x < TT; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[x][i] = exp2_fast(s[x][i] - ref[i & 1]);
-        l[e][i & 1] += s[x][i];
-      }
+      for (int i = 0; i < 4; i += 2) add_pair(s[x][i], s[x][i + 1], less[0], less[1]);
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[x][i] = exp2_fast(s[x][i]);
+#pragma unroll
+    for (int x = 0; x < TT; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) add_pair(l[e][0], l[e][1], s[x][i], s[x][i + 1]);
   }
 
   // The tokens 2t, 2t + 1, 2t + 8, 2t + 9 of tile x in the j-th chunk of columns; zeros where one does not count.

@@ -191,3 +191,9 @@ def test_slots_of_positions_outside_the_table():
         cache.slots(table[:, :0], torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError):
         cache.slots(table, torch.zeros(3, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("eps,rows", [(None, 4), ("1", 4), (1e-6, 4.5), (1e-6, None), (1e-6, 1 << 70)])
+def test_values_of_the_wrong_kind_are_type_errors(eps, rows):
+    with pytest.raises(TypeError, match="w4_rms_add"):
+        _lib.rms_add(P, 0, 0, rows, 64, eps, 0, P, 0)

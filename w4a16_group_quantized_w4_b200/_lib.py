@@ -118,7 +118,11 @@ def _packer(entry: int):
     n = len(args)
 
     def call(*values):
-        status = load().w4_packed(entry, block.pack(n, *values))
+        try:
+            words = block.pack(n, *values)
+        except struct.error as e:                # a value that is no number of its parameter's kind
+            raise TypeError(f"{_NAMES[entry]}: {e}") from None
+        status = load().w4_packed(entry, words)
         if status:
             raise W4Error(_NAMES[entry], status)
     return call

@@ -97,8 +97,9 @@ inline int64_t recs_bytes(int sms) { return (static_cast<int64_t>(sms) * kMostBl
 // 16-token tiles a stage, stages of a warp's ring and blocks per SM, by [whole][kind][head_dim / 64 - 1]: for
 // long streams, and for items that a block takes whole (short ones: more blocks hide the way to their first
 // bytes, and deep rings would not fill).  Swept: of int8, 128, 64 sequences to 8192 tokens, {1, 3, 3} takes 74 us,
-// {1, 2, 4} 84, {1, 3, 4} 97, {1, 4, 3} 117; of int4, 256, 48 windows of 16384, {1, 3, 3}
-// takes 58 us, {2, 2, 2} 61, {1, 4, 3} 78, {2, 3, 2} 80; bf16 wants the deepest rings that fit.
+// {1, 2, 4} 84, {2, 2, 2} 128 (four blocks of three stages do not fit an SM's shared memory); of int4, 128, 8 sequences
+// of 32768, {2, 3, 3} takes 83 us, {1, 5, 3} 90, {2, 4, 2} 92; of int4, 256, 48 windows of 16384, {1, 3, 3}, {1, 2, 3} and
+// {1, 4, 2} 57 to 58, {2, 2, 2} 61; bf16 wants the deepest rings that fit.
 struct Shape {
   int tiles, stages, blocks;
 };
@@ -142,6 +143,7 @@ struct Cfg {
   static constexpr int kStage = TT * kTileBytes;
   static constexpr int kJoin = kWarps * kHeads * (D + 4) * 4;
   static constexpr int kSmem = kWarps * S * kStage > kJoin ? kWarps * S * kStage : kJoin;
+  static_assert(MINB * (kSmem + 2048) <= 233472, "MINB blocks, with a KB of their own and one reserved each, fit an SM");
   // What beginning an item costs a block (its query, its first loads, its join), in units of tokens: about the
   // time in which an SM's share of the memory bandwidth brings 150 KB, divided among the SM's blocks.
   static constexpr int kUnitBytes = 2 * kUnit * (4 * ROWW + (KIND == W4_KV_BF16 ? 0 : 2 * NG));

@@ -197,3 +197,8 @@ def test_slots_of_positions_outside_the_table():
 def test_values_of_the_wrong_kind_are_type_errors(eps, rows):
     with pytest.raises(TypeError, match="w4_rms_add"):
         _lib.rms_add(P, 0, 0, rows, 64, eps, 0, P, 0)
+
+
+@pytest.mark.parametrize("q,out", [(P, P), (P, P + 1008), (P + 1008, P), (P + 512, P)])
+def test_attention_refuses_outputs_over_queries(q, out):
+    assert attend(_lib.load(), q=q, out=out) == BAD           # (two rows of 4 heads of 64: 1024 bytes each)

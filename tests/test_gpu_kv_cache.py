@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from oracle import bf16, decode
-from w4a16_group_quantized_w4_b200 import api
+from w4a16_group_quantized_w4_b200 import _lib, api
 from tests._util import dev_bf16, host_bf16_bits, host_f64, host_u32
 
 pytestmark = pytest.mark.gpu
@@ -351,6 +351,18 @@ def test_same_bits_every_time_and_on_another_stream(kind):
     outs += [s.cache.attend(q, s.table_d, s.lens_d) for _ in range(3)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, first) for o in outs)
+
+
+def test_output_beside_the_queries_but_not_over_them():
+    s = Seqs([40, 300], 2, 64, 16, "int8", 3)
+    rows = torch.randn((4, 4, 64), device="cuda").to(torch.bfloat16)
+    want = s.cache.attend(rows[:2].clone(), s.table_d, s.lens_d)
+    with pytest.raises(_lib.W4Error):
+        s.cache.attend(rows[:2], s.table_d, s.lens_d, out=rows[1:3])
+    got = s.cache.attend(rows[:2], s.table_d, s.lens_d, out=rows[2:])
+    assert torch.equal(got, want)
+    other = s.cache.attend(rows[2:], s.table_d, s.lens_d, out=rows[:2])
+    assert other.data_ptr() == rows.data_ptr()
 
 
 @pytest.mark.parametrize("kind", KINDS)

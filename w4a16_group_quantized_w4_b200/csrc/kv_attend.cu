@@ -34,6 +34,10 @@ extern "C" w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const 
   if (workspace_bytes < w4_workspace_bytes(W4_OP_ATTEND, B, q_heads, head_dim, kv_heads, 0) ||
       (!workspace && w4_workspace_bytes(W4_OP_ATTEND, B, q_heads, head_dim, kv_heads, 0)))
     return W4_ERR_WORKSPACE;
+  // blocks write their heads while others still read theirs
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const uint64_t row = static_cast<uint64_t>(q_heads) * head_dim * 2;
+  if (o0 < q0 + static_cast<uint64_t>(B - 1) * q_stride * 2 + row && q0 < o0 + B * row) return W4_ERR_INVALID_ARG;
   at::Args a{};
   a.q = q;
   a.q_stride = q_stride;

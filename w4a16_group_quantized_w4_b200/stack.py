@@ -156,7 +156,8 @@ class MoEStack:
         logits[l] f32 [T, E], around the residual stream that x0 bf16 [T, H] begins.  Returns
         (norm of the final residual stream with weight `norm`, the stream), both bf16 [T, H].  Rows whose
         slot is negative and whose length is 0 are padding.  The expert layers share scratch and keep their
-        buffers: two steps must not overlap on the GPU, nor two captured ones be replayed at once."""
+        buffers (allocated by the first step of a T and path: run one before capturing one): two steps must
+        not overlap on the GPU, nor two captured ones be replayed at once."""
         if len(blocks) != self.L:
             raise ValueError(f"blocks: expected {self.L}, got {len(blocks)}")
         T = x0.shape[0]

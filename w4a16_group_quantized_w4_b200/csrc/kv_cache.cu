@@ -208,14 +208,15 @@ __device__ __forceinline__ Raw<KIND> load_row8(const Chunk& k, int dim, const vo
   return r;
 }
 
-// A code's bits u = q + bias in the second byte of 2^15 (0x4700uu00) are the float 2^15 + u.  (2^15 + bias) *
-// scale has 17 significant bits at most, so one fused multiply-add gives q * scale exactly; bf16 rounds it once.
+// A code's bits u = q + bias in the second byte of 2^15 (0x4700uu00) are the float 2^15 + u.  Less 2^15 + bias it is
+// q, and q * scale has 16 significant bits at most: both steps are exact whatever the scale (one fused step with
+// (2^15 + bias) * scale as addend would overflow from scales of 2^113 on), and bf16 rounds once.
 template <int KIND>
 __device__ __forceinline__ uint4 values8(const Raw<KIND>& r) {
   if constexpr (KIND == W4_KV_BF16) {
     return make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
   } else {
-    const float s = bf16_lo_to_f32(r.scale), off = -(32768.f + (KIND == W4_KV_INT8 ? 128.f : 8.f)) * s;
+    const uint64_t s2 = twice(bf16_lo_to_f32(r.scale)), off2 = twice(-(32768.f + (KIND == W4_KV_INT8 ? 128.f : 8.f)));
     uint32_t u[2];                                        // bytes: elements 0..3, 4..7 (int8), even, odd (int4)
     if constexpr (KIND == W4_KV_INT8) {
       u[0] = r.w[0] ^ 0x80808080u;
@@ -226,10 +227,19 @@ __device__ __forceinline__ uint4 values8(const Raw<KIND>& r) {
     }
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t word = KIND == W4_KV_INT8 ? u[j >> 2] : u[j & 1];
-      const int byte = KIND == W4_KV_INT8 ? j & 3 : j >> 1;
-      f[j] = fmaf(__uint_as_float(__byte_perm(word, 0x47000000u, 0x7404 | byte << 4)), s, off);
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t word = KIND == W4_KV_INT8 ? u[j >> 2] : u[i];
+        const int byte = KIND == W4_KV_INT8 ? (j + i) & 3 : j >> 1;
+        b[i] = __byte_perm(word, 0x47000000u, 0x7404 | byte << 4);
+      }
+      uint64_t x;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(b[0]), "r"(b[1]));
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(off2));
+      asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(s2));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(f[j]), "=f"(f[j + 1]) : "l"(x));
     }
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   }

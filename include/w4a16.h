@@ -395,7 +395,8 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  *   head_dim 64, 128, 192 or 256 (W4_ERR_UNSUPPORTED otherwise); any page_size >= 1;
  *   q_heads % kv_heads == 0; table_width * page_size < 2^31 - 4096 and, times q_heads, below
  *   2^36; pages * kv_heads * page_size < 2^32 (W4_ERR_UNSUPPORTED beyond).
- * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.  Weights enter the sum over
+ * Scores, maxima, sums and outputs are float32; out is rounded once to bf16.  A softcap up to 64 is applied within
+ * 2^-21 of itself, a larger one within 2^-20 of the capped score.  Weights enter the sum over
  * bf16 values with 16 bits; over int8 and int4 values weights and scaled values enter it in fp16, rounded to
  * 11 bits.  Weights below 2^-20 of the sequence's largest keep fewer; so do values, an error of 2^-20 of the
  * largest scale that meets the same output element being possible, and, against an int8 or int4 cache, elements

@@ -33,3 +33,108 @@ def test_rows_of_every_size_are_read_back_whole(kind):
         q, s = decode.quantise_rows(x.reshape(-1, dim), kind)
         assert bf16.to_f64(s).max() > 2.0 ** 118
         assert np.array_equal(host_bf16_bits(got).reshape(T, dim), bf16.from_f64(decode.row_values(q, s)))
+
+
+class Filled:
+    """Sequences of given lengths over rows that the caller makes: k, v bf16 bits [sum of lens, heads, dim]."""
+
+    def __init__(self, lens, k, v, page, kind, seed=0):
+        r = np.random.RandomState(seed)
+        _, heads, dim = k.shape
+        need = [-(-n // page) for n in lens]
+        pages = sum(need) + 1
+        order = r.permutation(pages)
+        table = np.full((len(lens), max(1, max(need))), -1, np.int32)
+        slots, at = [], 0
+        for b, n in enumerate(lens):
+            table[b, :need[b]] = order[at:at + need[b]]
+            at += need[b]
+            pos = np.arange(n)
+            slots.append(table[b, pos // page].astype(np.int64) * page + pos % page)
+        slots = np.concatenate(slots)
+        self.lens, self.heads, self.dim, self.kind = lens, heads, dim, kind
+        self.cache = api.KVCache(pages, heads, page, dim, kind)
+        self.cache.write(dev_bf16(k), dev_bf16(v), torch.from_numpy(slots).cuda())
+        cut = np.cumsum(lens)[:-1]
+        self.k, self.v, self.ks = [], [], []
+        for x, out in ((k, self.k), (v, self.v)):
+            if kind == "bf16":
+                f, s = bf16.to_f64(x), np.zeros((len(x), heads, dim))
+            else:
+                q, sb = decode.quantise_rows(x.reshape(-1, dim), kind)
+                f = decode.row_values(q, sb).reshape(x.shape)
+                s = np.repeat(bf16.to_f64(sb), 32, axis=1).reshape(x.shape)
+            out.extend(np.split(f, cut))
+            if out is self.k:
+                self.ks = np.split(s, cut)               # a key element's scale (0: none)
+        self.table = torch.from_numpy(table).cuda()
+        self.lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def attend(self, q, **kw):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = self.cache.attend(dev_bf16(q), self.table, self.lens_d, lse=lse, dev_status=st, **kw)
+        assert st.item() == 0
+        return host_f64(out), lse.cpu().numpy().astype(np.float64)
+
+    def check(self, q, scale=None, softcap=0.0, window=0):
+        """Scores: a group's products and its bias (128 scales an element, int8; 8, int4) are summed in float32 in
+        at most dim / 16 + dim / 32 + 5 steps, each off by 2^-22 of the magnitudes in it (a tensor-core step may
+        cut off where float32 would round); a cap adds 2^-20 of the score, or, up to 64, 2^-21 of
+        itself (2^x within 2^-22, a reciprocal within 2^-23)."""
+        out, lse = self.attend(q, scale=scale, softcap=softcap, window=window)
+        scale = self.dim ** -0.5 if scale is None else scale
+        qf, G = bf16.to_f64(q), q.shape[1] // self.heads
+        bias = {"bf16": 0.0, "int8": 128.0, "int4": 8.0}[self.kind]
+        steps = self.dim / 16 + self.dim / 32 + 5
+        for b, n in enumerate(self.lens):
+            seen = slice(max(0, n - window) if window else 0, n)
+            for h in range(q.shape[1]):
+                k, v, ks = (x[b][seen, h // G] for x in (self.k, self.v, self.ks))
+                ref, ref_lse, mag, _, vsum = decode.attend(qf[b, h], k, v, scale, softcap)
+                if n == 0:
+                    assert lse[b, h] == -np.inf and not out[b, h].any()
+                    continue
+                size = np.max((np.abs(k) + 2 * bias * ks) @ np.abs(qf[b, h])) * abs(scale)
+                dz = steps * 2.0 ** -22 * size + 2.0 ** -22
+                if softcap:
+                    dz += 2.0 ** -21 * softcap if softcap <= 64 else 2.0 ** -20 * np.abs(k @ qf[b, h]).max() * abs(scale)
+                assert abs(lse[b, h] - ref_lse) <= dz + 2.0 ** -17 + abs(ref_lse) * 2.0 ** -22, (b, h, lse[b, h] - ref_lse, dz)
+                tol = np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -9 + 2 * dz) + 2.0 ** -31 * vsum
+                assert (np.abs(out[b, h] - ref) <= tol).all(), (b, h, np.abs(out[b, h] - ref).max())
+
+
+def normal(r, *shape):
+    return r.randn(*shape) * np.exp(0.5 * r.randn(*shape[1:]))
+
+
+LENS = [1, 0, 17, 130, 1500]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("softcap", [1e-3, 50.0, 64.0, 65.0, 300.0, 1e4, 1e6, 1e8, 1e20, 1e38, 3.4e38])
+def test_caps_of_every_size(kind, softcap):
+    """Scores far below the cap come out as they went in, to float32's last places."""
+    r = np.random.RandomState(3)
+    k, v = (bf16.from_f64(normal(r, sum(LENS), 2, 64)) for _ in range(2))
+    Filled(LENS, k, v, 16, kind).check(bf16.from_f64(r.randn(len(LENS), 6, 64)), softcap=softcap)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,q_heads", [(128, 12), (256, 4)])
+@pytest.mark.parametrize("scale", [1.0, 6.0])
+def test_scores_around_a_large_cap(kind, dim, q_heads, scale):
+    """Scores on both sides of half the cap, where the way to tanh changes, and far past it."""
+    r = np.random.RandomState(4)
+    k, v = (bf16.from_f64(normal(r, 700, 1, dim)) for _ in range(2))
+    Filled([650, 50], k, v, 16, kind).check(bf16.from_f64(r.randn(2, q_heads, dim)), scale=scale, softcap=100.0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page", [1, 24, 64])
+@pytest.mark.parametrize("window", [0, 1, 100])
+def test_large_caps_over_pages_and_windows(kind, page, window):
+    r = np.random.RandomState(page)
+    lens = [0, 1, 70, 333, 64]
+    k, v = (bf16.from_f64(normal(r, sum(lens), 2, 192)) for _ in range(2))
+    Filled(lens, k, v, page, kind).check(bf16.from_f64(r.randn(len(lens), 6, 192)), softcap=1e5, window=window)

@@ -245,11 +245,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// tanh(y ln 2 / 2) = 1 - 2 / (2^y + 1), off by about 2^-22 of 1
+// tanh(y ln 2 / 2) = 1 - 2 / (2^y + 1), off by 2^-21 of 1 at most
 __device__ __forceinline__ float tanh_fast(float y) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(y) + 1.f));
   return fmaf(-2.f, r, 1.f);
+}
+// Up to this cap the whole of tanh_fast's error is 2^-15 of a score at most.  A larger cap would make it as much
+// larger while the scores may be as small as ever: those calls have kernels of their own (WIDE), which
+// need not be fast.  (The choice inside the loop cost every call: one short sequence 6.2 us, not 5.6, or 16
+// capped bf16 sequences of 8192 tokens 93 us, not 90.)
+constexpr float kFastCap = 64.f;
+// cap tanh(s / cap) within a few float32 roundings of itself; in = 2 / softcap for s and cap in log2 units.  Below half
+// the cap by tanh's Taylor series (its terms fall by 0.1 there, the first left out is 2^-23 of the sum), as a factor
+// of s, so that scores far below the cap keep all their bits.
+__device__ __forceinline__ float cap_exactly(float s, float cap, float in) {
+  const float y = s * in, x = y * 0.34657359028f, x2 = x * x;
+  float p = fmaf(x2, 21844.f / 6081075.f, -1382.f / 155925.f);
+  p = fmaf(p, x2, 62.f / 2835.f);
+  p = fmaf(p, x2, -17.f / 315.f);
+  p = fmaf(p, x2, 2.f / 15.f);
+  p = fmaf(p, x2, -1.f / 3.f);
+  return fabsf(x) < 0.5f ? fmaf(s * x2, p, s) : cap * tanh_fast(y);
 }
 
 // Float32 pairs, both elements in one instruction: (a, b) *= (c, d), += (c, d), += (c, d) f.  (Scores, weights and
@@ -305,7 +322,7 @@ __device__ __forceinline__ float log_sum(float m, float l, float lift) {
   return l > 0.f ? (m - lift + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int KIND, int D, int HT, bool U16, bool WHOLE>
+template <int KIND, int D, int HT, bool U16, bool WHOLE, bool WIDE>
 struct Worker {
   using C = Cfg<KIND, D, HT, WHOLE>;
   static constexpr bool kBf = KIND == W4_KV_BF16;
@@ -584,8 +601,14 @@ struct Worker {
     for (int x = 0; x < TT; ++x)
 #pragma unroll
       for (int i = 0; i < 4; i += 2) mul_pair(s[x][i], s[x][i + 1], zmul[e][0], zmul[e][1]);
-    if (a.softcap > 0.f) {
-      // cap(z) = softcap tanh(z / softcap), in log2 units on both sides
+    // cap(z) = softcap tanh(z / softcap), in log2 units on both sides
+    if constexpr (WIDE) {
+      const float cap = fminf(a.softcap * 1.4426950408889634f, 3.4028234e38f), in = 2.f / a.softcap;
+#pragma unroll
+      for (int x = 0; x < TT; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] = cap_exactly(s[x][i], cap, in);
+    } else if (a.softcap > 0.f) {
       const float cap = a.softcap * 1.4426950408889634f, in = 2.f / a.softcap;
 #pragma unroll
       for (int x = 0; x < TT; ++x)
@@ -833,8 +856,8 @@ struct Worker {
   }
 };
 
-// WHOLE: block x takes item x as it is.  Otherwise the blocks share the line evenly.
-template <int KIND, int D, int HT, bool U16, bool WHOLE>
+// WHOLE: block x takes item x as it is.  Otherwise the blocks share the line evenly.  WIDE: caps above kFastCap.
+template <int KIND, int D, int HT, bool U16, bool WHOLE, bool WIDE>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, HT, WHOLE>::MINB) attend_kernel(const Args a) {
   using C = Cfg<KIND, D, HT, WHOLE>;
   constexpr int kHeads = C::kHeads;
@@ -922,7 +945,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, HT, WHOLE>::MINB) at
   const int64_t start_at = at;
   const int start_n = sp.n;
 
-  Worker<KIND, D, HT, U16, WHOLE> w(a);
+  Worker<KIND, D, HT, U16, WHOLE, WIDE> w(a);
   w.ring = smem_u32(s_ring) + warp * (C::S * C::kStage);
   w.marks = s_marks[warp];
   while (true) {
@@ -1093,10 +1116,11 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
 // Otherwise as many blocks as the SMs hold, or one a unit if there are fewer, share the line.
 constexpr int kShort = 6, kLittle = 8, kMiddling = 64;
 
-template <int KIND, int D, int HT, bool WHOLE>
+template <int KIND, int D, int HT, bool WHOLE, bool WIDE>
 w4_status launch_mode(const Args& a, int grid, cudaStream_t s) {
-  const bool u16 = a.page_size % 16 == 0;
-  auto kernel = u16 ? attend_kernel<KIND, D, HT, true, WHOLE> : attend_kernel<KIND, D, HT, false, WHOLE>;
+  // (a wide cap's kernel takes all page sizes token by token)
+  const bool u16 = !WIDE && a.page_size % 16 == 0;
+  auto kernel = u16 ? attend_kernel<KIND, D, HT, !WIDE, WHOLE, WIDE> : attend_kernel<KIND, D, HT, false, WHOLE, WIDE>;
   constexpr int kSmem = Cfg<KIND, D, HT, WHOLE>::kSmem;
   static SmemRaised raised[2];
   if (raise_smem(kernel, kSmem, raised[u16]) != cudaSuccess) return W4_ERR_CUDA;
@@ -1114,10 +1138,12 @@ w4_status launch_heads(Args a, cudaStream_t s, int sms) {
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * a.HB;
   const int64_t units = (static_cast<int64_t>(a.table_width) * a.page_size + kUnit - 1) / kUnit;
   int64_t most = static_cast<int64_t>(sms) * Cfg<KIND, D, HT, false>::MINB;
-  if (units <= kShort || (units <= kLittle && items >= most) || (units <= kMiddling && items >= 4 * most))
-    return launch_mode<KIND, D, HT, true>(a, static_cast<int>(items), s);
+  const bool wide = a.softcap > kFastCap;
+  if (!wide && (units <= kShort || (units <= kLittle && items >= most) || (units <= kMiddling && items >= 4 * most)))
+    return launch_mode<KIND, D, HT, true, false>(a, static_cast<int>(items), s);
   most = most < kMostGrid ? most : kMostGrid;
-  return launch_mode<KIND, D, HT, false>(a, static_cast<int>(items * units < most ? items * units : most), s);
+  const int grid = static_cast<int>(items * units < most ? items * units : most);
+  return wide ? launch_mode<KIND, D, HT, false, true>(a, grid, s) : launch_mode<KIND, D, HT, false, false>(a, grid, s);
 }
 
 template <int KIND, int D>

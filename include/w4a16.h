@@ -401,6 +401,7 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  * 11 bits.  Weights below 2^-20 of the sequence's largest keep fewer; so do values, an error of 2^-20 of the
  * largest scale that meets the same output element being possible, and, against an int8 or int4 cache, elements
  * of q below 2^-24 of their head's largest.
+ * Weights reach 2^8 in a sum over bf16 values: |v| times the tokens of a sequence has to stay below 2^119 there.
  * Rows of the cache that no sequence's (windowed) length covers are never looked at.
  */
 w4_status kv_cache_attend(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,

@@ -138,3 +138,16 @@ def test_large_caps_over_pages_and_windows(kind, page, window):
     lens = [0, 1, 70, 333, 64]
     k, v = (bf16.from_f64(normal(r, sum(lens), 2, 192)) for _ in range(2))
     Filled(lens, k, v, page, kind).check(bf16.from_f64(r.randn(len(lens), 6, 192)), softcap=1e5, window=window)
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("dim,q_heads", [(64, 4), (128, 12), (256, 3)])
+def test_values_at_the_end_of_the_range(kind, dim, q_heads):
+    """Groups whose scales are among the largest that finite rows have (2^120, int8; 2^125, int4), among smaller ones;
+    items that a block holds whole, and cut ones."""
+    r = np.random.RandomState(dim)
+    lens = [1, 40, 0, 3000]
+    k = bf16.from_f64(normal(r, sum(lens), 1, dim))
+    v = r.uniform(0.5, 1.0, (sum(lens), 1, dim)) * r.choice([-1, 1], (sum(lens), 1, dim))
+    v *= 3.3e38 * 2.0 ** -r.randint(0, 6, (sum(lens), 1, dim // 32)).repeat(32, axis=2)
+    Filled(lens, k, bf16.from_f64(v), 16, kind).check(bf16.from_f64(r.randn(len(lens), q_heads, dim)))

@@ -57,7 +57,7 @@ struct Args {
   int window;
   uint16_t* out;
   float* lse;
-  float* parts;                       // [2 * grid][heads * (D + 2)]: sums, references, totals of an item's heads
+  float* parts;                       // [2 * grid][heads * (D + 2)]: outputs, references, totals of an item's heads
   Rec* recs;                          // [grid]
   int32_t* dev_status;
   // derived
@@ -317,6 +317,14 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// What sums of weighted values are multiplied by, l being the sum of the weights: at least 1, or 0 for no token.
+// Every partial output (a warp's, a block's) is divided by its own weights' sum, so that no step leaves the range
+// of the values themselves: sums of weights reach 2^14 times the tokens.
+__device__ __forceinline__ float inverse_of(float l) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
+  return l == 0.f ? 0.f : y;
+}
 // the logarithm of a sum of weights taken relative to m, less the lift
 __device__ __forceinline__ float log_sum(float m, float l, float lift) {
   return l > 0.f ? (m - lift + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -962,7 +970,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, HT, WHOLE>::MINB) at
     if (take > 0) {
       w.walk(max(t0, w.lo & ~15), warp, head0, heads);
 
-      // join the warps: head h's reference is the largest of theirs
+      // join the warps: head h's reference is the largest of theirs, their shares go by their weights
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 2 * HT; ++i) {
@@ -974,41 +982,49 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<KIND, D, HT, WHOLE>::MINB) at
           s_l[warp][8 * e + 2 * w.t + c] = w.l[e][c];
         }
       }
-      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop<KIND>);
+      // (2^kMore goes to the other factor: an exponent stays below 127)
+      constexpr int kMore = KIND == W4_KV_INT4 ? 8 : 0;
+      const float unit = KIND == W4_KV_BF16 ? 1.f : pow2f(w.vexp - 127 - kScaleTop<KIND> - kMore);
 #pragma unroll
-      for (int e = 0; e < HT; ++e)
+      for (int e = 0; e < HT; ++e) {
+        const float inv0 = inverse_of(w.l[e][0]) * (1 << kMore), inv1 = inverse_of(w.l[e][1]) * (1 << kMore);
 #pragma unroll
         for (int j = 0; j < C::NV; ++j)
 #pragma unroll
           for (int i = 0; i < C::VE / 2; ++i) {
             const float* o = w.acc[e][j * C::VE / 2 + i];
             const int d = j * 8 * C::VE + w.r * C::VE + 2 * i;
-            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t][d]) = make_float2(o[0] * unit, o[2] * unit);
-            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t + 1][d]) = make_float2(o[1] * unit, o[3] * unit);
+            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t][d]) = make_float2(o[0] * inv0 * unit, o[2] * inv0 * unit);
+            *reinterpret_cast<float2*>(&s_o[warp][8 * e + 2 * w.t + 1][d]) = make_float2(o[1] * inv1 * unit, o[3] * inv1 * unit);
           }
+      }
       __syncthreads();
       const bool whole = take == sp.n;
       // a block continues an item in its slot 0 and begins one in its slot 1
       float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (u > 0 ? 0 : 1)) * kHeads * (D + 2);
       for (int x = threadIdx.x; x < heads * (D / 4); x += 32 * kWarps) {
         const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
-        float mm = kLowest, ll = 0.f;
+        float mm = kLowest, ll = 0.f, part_l[kWarps];
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s_m[k][h]);
+#pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-          const float f = exp2_fast(s_m[k][h] - mm);
+          part_l[k] = exp2_fast(s_m[k][h] - mm) * s_l[k][h];
+          ll += part_l[k];
+        }
+        const float inv = inverse_of(ll);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float f = part_l[k] * inv;
           const float4 v = *reinterpret_cast<const float4*>(&s_o[k][h][d]);
-          ll = fmaf(f, s_l[k][h], ll);
           o.x = fmaf(f, v.x, o.x);
           o.y = fmaf(f, v.y, o.y);
           o.z = fmaf(f, v.z, o.z);
           o.w = fmaf(f, v.w, o.w);
         }
         if (whole) {
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
           const int64_t row = static_cast<int64_t>(b) * a.q_heads + head0 + h;
-          *reinterpret_cast<uint2*>(a.out + row * D + d) =
-              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
           if (a.lse && d == 0)
             a.lse[row] = log_sum(mm, ll, KIND == W4_KV_BF16 ? 0.f : kLift);
         } else {
@@ -1078,14 +1094,15 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
   m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   float l = 0.f;
   for (int i = threadIdx.x; i < n; i += 128) {
-    s_f[i] = exp2_fast(s_f[i] - m);
-    l = fmaf(s_f[i], s_t[i], l);
+    s_f[i] = exp2_fast(s_f[i] - m) * s_t[i];
+    l += s_f[i];
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
   l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const float inv = inverse_of(l);
   float o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
@@ -1095,15 +1112,14 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a, float lift) {
     for (int x = 0; x < kBatch; ++x)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i0 + 4 * x < n) o[i] = fmaf(v[x][i], s_f[i0 + 4 * x], o[i]);
+        if (i0 + 4 * x < n) o[i] = fmaf(v[x][i], s_f[i0 + 4 * x] * inv, o[i]);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
   __syncthreads();
-  const float inv = l > 0.f ? 1.f / l : 0.f;
   const int64_t row = static_cast<int64_t>(rec.b) * a.q_heads + hk * a.G + hb * kHeads + h;
   for (int d = threadIdx.x; d < D; d += 128)
-    a.out[row * D + d] = f32_to_bf16_bits(((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) * inv);
+    a.out[row * D + d] = f32_to_bf16_bits((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]));
   if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(m, l, lift);
 }
 

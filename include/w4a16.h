@@ -400,7 +400,7 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  * bf16 values with 16 bits; over int8 and int4 values weights and scaled values enter it in fp16, rounded to
  * 11 bits.  Weights below 2^-20 of the sequence's largest keep fewer; so do values, an error of 2^-20 of the
  * largest scale that meets the same output element being possible, and, against an int8 or int4 cache, elements
- * of q below 2^-24 of their head's largest.
+ * of q below 2^-24 of their head's largest (scale * |q| has to stay below 2^116 there).
  * Weights reach 2^8 in a sum over bf16 values: |v| times the tokens of a sequence has to stay below 2^119 there.
  * Rows of the cache that no sequence's (windowed) length covers are never looked at.
  */

@@ -151,3 +151,28 @@ def test_values_at_the_end_of_the_range(kind, dim, q_heads):
     v = r.uniform(0.5, 1.0, (sum(lens), 1, dim)) * r.choice([-1, 1], (sum(lens), 1, dim))
     v *= 3.3e38 * 2.0 ** -r.randint(0, 6, (sum(lens), 1, dim // 32)).repeat(32, axis=2)
     Filled(lens, k, bf16.from_f64(v), 16, kind).check(bf16.from_f64(r.randn(len(lens), q_heads, dim)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,q_heads", [(64, 4), (128, 12)])
+@pytest.mark.parametrize("size", [-113, -105, -60, 90, 100, 110, 119])
+def test_ordinary_scores_of_large_and_small_keys(kind, dim, q_heads, size):
+    """Keys of about 2^size under queries of about 2^-size: a sum in front of the last factor may leave float32's
+    range although no score does."""
+    r = np.random.RandomState(dim)
+    lens = [1, 33, 700]
+    k = bf16.from_f64(np.clip(normal(r, sum(lens), 1, dim) * 2.0 ** size, -3e38, 3e38))
+    v = bf16.from_f64(normal(r, sum(lens), 1, dim))
+    q = r.randn(len(lens), q_heads, dim) * 2.0 ** -size
+    Filled(lens, k, v, 16, kind).check(bf16.from_f64(np.clip(q, -3e38, 3e38)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [-126, -100, 0, 110])
+def test_heads_of_unlike_sizes_beside_one_another(kind, size):
+    """Query heads of one item whose elements lie 2^20 to 2^120 apart."""
+    r = np.random.RandomState(9)
+    lens = [40, 200]
+    k, v = (bf16.from_f64(normal(r, sum(lens), 1, 128) * s) for s in (2.0 ** -115, 1.0))
+    q = r.randn(2, 20, 128) * 2.0 ** np.tile([115.0, 116, 117, 95, size], 4)[:, None]
+    Filled(lens, k, v, 16, kind).check(bf16.from_f64(np.clip(q, -3e38, 3e38)))

@@ -198,16 +198,17 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
 // of a subnormal number; the bias leaves again in float32 (keys: by products of scales and sums of q) or in the
 // fused multiply by the scale (values), where it must be exact in fp16 after that multiplication.
 //
-// Keys, int8: bytes offset by 128, 0x6400 | u = 1024 + u = 1152 + code.
+// Keys, int8: bytes offset by 128, the subnormal u 2^-24 with u = code + 128.  (On 1024 instead, a group's
+// product would reach 2^31, and scales from 2^98 on would take it out of float32's range.)
 template <int SEL>
-__device__ __forceinline__ uint32_t key_bytes(uint32_t v) { return __byte_perm(v, 0x64646464u, SEL); }
+__device__ __forceinline__ uint32_t key_bytes(uint32_t v) { return __byte_perm(v, 0u, SEL); }
 // int4: a nibble at bits 0..3 of a half is the subnormal u 2^-24, at bits 4..7 u 2^-20, with u = code + 8:
 // one AND each, and a single shift by 8 for the other two nibbles of the half.
 __device__ __forceinline__ uint32_t nib0(uint32_t v) { return v & 0x000F000Fu; }
 __device__ __forceinline__ uint32_t nib1(uint32_t v) { return v & 0x00F000F0u; }
 // what a key product's bias is, per unit of the queries' sum
 template <int KIND>
-constexpr float kKeyBias = KIND == W4_KV_INT8 ? 1152.f : 8.f / 16777216.f;
+constexpr float kKeyBias = (KIND == W4_KV_INT8 ? 128.f : 8.f) / 16777216.f;
 // Values, int8: bytes sign-extended to 16 bits, (b & 0x3FF) ^ 0x6600 = 1536 + code; 1536 = 3 * 512, so
 // 1536 * scale has 10 significant bits at most and fma(x, s, -1536 s) is code * s rounded once.
 template <int SEL>
@@ -395,7 +396,7 @@ struct Worker {
         }
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int f = shift_for(mx, 14);
+      const int f = mx ? min(14 + 127 - static_cast<int>(max(mx >> 7, 1u)), 126) : 0;   // -113 at least
       const float up = pow2f(f);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -431,7 +432,7 @@ struct Worker {
         bias[0] -= bf16_lo_to_f32(qb[e][i]);
         bias[1] -= bf16_hi_to_f32(qb[e][i]);
       }
-      const float down = base * pow2f(-f) * (KIND == W4_KV_INT4 ? 16777216.f : 1.f);
+      const float down = base * pow2f(-f) * 16777216.f;      // (the keys' 2^-24 is taken back too)
       zmul[e][0] = __shfl_sync(0xffffffffu, down, 8 * t);
       zmul[e][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }

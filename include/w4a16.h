@@ -386,7 +386,8 @@ w4_status kv_cache_read(const int64_t* slots, int64_t T, int32_t kind, int32_t k
  *              been written); 0 gives out = 0 and lse = -infinity.
  *   window     0, or w > 0: only the last w tokens are seen.
  *   out        [B, q_heads, head_dim] bf16 (W4_ERR_INVALID_ARG where it overlaps q).
- *   lse        [B, q_heads] float32 or NULL: log sum exp(score).
+ *   lse        [B, q_heads] float32 or NULL: log sum exp(score).  A score of NaN or +infinity (a NaN in
+ *              q, in a key row or in a key scale that the sequence sees) makes out and lse of its heads NaN.
  *   workspace  at least w4_workspace_bytes(W4_OP_ATTEND, B, q_heads, head_dim, kv_heads, 0) bytes,
  *              16-byte aligned; contents need no preparation.  Calls sharing it must not overlap.
  *   dev_status one int32 device word or NULL: W4_ERR_INVALID_ARG when a length is negative (taken as

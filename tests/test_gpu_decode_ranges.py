@@ -176,3 +176,45 @@ def test_heads_of_unlike_sizes_beside_one_another(kind, size):
     k, v = (bf16.from_f64(normal(r, sum(lens), 1, 128) * s) for s in (2.0 ** -115, 1.0))
     q = r.randn(2, 20, 128) * 2.0 ** np.tile([115.0, 116, 117, 95, size], 4)[:, None]
     Filled(lens, k, v, 16, kind).check(bf16.from_f64(np.clip(q, -3e38, 3e38)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,heads,q_heads", [(64, 2, 4), (128, 2, 24)])
+def test_nan_reaches_the_output_and_lse_of_its_heads_alone(kind, dim, heads, q_heads):
+    """A NaN query, and a cached key that held an infinity (a group of NaN; an infinity in a bf16 cache), in a short
+    sequence and in a long one that is cut: out and lse are NaN, not the -infinity of an empty sequence."""
+    r = np.random.RandomState(dim)
+    lens = [20, 3000, 1, 20, 3000, 0]
+    G = q_heads // heads
+    k, v = (bf16.from_f64(normal(r, sum(lens), heads, dim)) for _ in range(2))
+    q = bf16.from_f64(r.randn(len(lens), q_heads, dim))
+    clean = Filled(lens, k, v, 16, kind).attend(q)
+    start = np.cumsum([0] + lens)
+    for b, token in ((0, 7), (1, 1700)):
+        k[start[b] + token, 1, dim - 3] = 0x7FC0 if kind == "bf16" else 0x7F80
+    q[3, 1, 5], q[4, G + 1, 0] = 0x7FC0, 0xFFC1
+    out, lse = Filled(lens, k, v, 16, kind).attend(q)
+    bad = np.zeros(lse.shape, bool)
+    bad[0, G:] = bad[1, G:] = True
+    bad[3, 1] = bad[4, G + 1] = True
+    assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+    # (the others' references may be raised at other tokens: weights within fp16's rounding)
+    assert (np.abs(out - clean[0])[~bad] <= 2.0 ** -7 * np.abs(clean[0][~bad]) + 2.0 ** -8 * np.abs(bf16.to_f64(v)).max()).all()
+    both = ~bad & (lse > -np.inf)
+    assert (np.abs(lse[both] - clean[1][both]) <= 2.0 ** -16).all()
+    assert np.isneginf(lse[5]).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_nan_values_leave_lse_alone(kind):
+    r = np.random.RandomState(6)
+    lens = [20, 3000]
+    k, v = (bf16.from_f64(normal(r, sum(lens), 1, 64)) for _ in range(2))
+    q = bf16.from_f64(r.randn(2, 4, 64))
+    clean = Filled(lens, k, v, 16, kind).attend(q)
+    size = np.abs(bf16.to_f64(v)).max()
+    v[[3, 20 + 1700], 0, 40] = 0x7FC0
+    out, lse = Filled(lens, k, v, 16, kind).attend(q)
+    gone = slice(40, 41) if kind == "bf16" else slice(32, 64)
+    assert np.isnan(out[:, :, gone]).all() and np.array_equal(lse, clean[1])
+    assert (np.abs(out - clean[0])[:, :, :32] <= 2.0 ** -7 * np.abs(clean[0][:, :, :32]) + 2.0 ** -8 * size).all()

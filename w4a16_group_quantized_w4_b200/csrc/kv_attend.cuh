@@ -326,9 +326,9 @@ __device__ __forceinline__ float inverse_of(float l) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
   return l == 0.f ? 0.f : y;
 }
-// the logarithm of a sum of weights taken relative to m, less the lift
+// the logarithm of a sum of weights taken relative to m, less the lift (NaN of a NaN sum: -infinity says no token)
 __device__ __forceinline__ float log_sum(float m, float l, float lift) {
-  return l > 0.f ? (m - lift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return l == 0.f ? -INFINITY : (m - lift + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int KIND, int D, int HT, bool U16, bool WHOLE, bool WIDE>

@@ -310,8 +310,8 @@ w4_status w4a16_linear_noalloc(const uint16_t* x, const uint32_t* codes, const u
  *              q_scale = max|y| / 127 per row and q = rint(y / q_scale).  A row of zeros gives scale
  *              0 and codes 0; a row holding NaN or infinity gives scale NaN and codes 0.
  *   T >= 0, H % 8 == 0, 8 <= H <= 32768 (W4_ERR_UNSUPPORTED above), eps >= 0.  q 8-byte aligned.
- * The norm is that of the stored (rounded) h.  The sum of squares is float32 in a fixed order, so
- * |h| beyond about 2^63 overflows it (y = 0, as in moe_rms_chain; scale NaN); codes can differ from exact
+ * The norm is that of the stored (rounded) h, however small; with eps = 0 a row of zeros gives zeros.  The sum
+ * of squares is float32 in a fixed order, so |h| beyond about 2^63 overflows it (y = 0, as in moe_rms_chain; scale NaN); codes can differ from exact
  * arithmetic by one where y / q_scale is within float32 rounding of a half.
  */
 w4_status w4_rms_add(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T,

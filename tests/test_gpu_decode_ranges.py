@@ -218,3 +218,64 @@ def test_nan_values_leave_lse_alone(kind):
     gone = slice(40, 41) if kind == "bf16" else slice(32, 64)
     assert np.isnan(out[:, :, gone]).all() and np.array_equal(lse, clean[1])
     assert (np.abs(out - clean[0])[:, :, :32] <= 2.0 ** -7 * np.abs(clean[0][:, :, :32]) + 2.0 ** -8 * size).all()
+
+
+@pytest.mark.parametrize("T,H,residual", [(1, 64, False), (3, 512, True), (300, 2816, True), (2, 32768, False), (2, 8200, True)])
+def test_rows_without_eps(T, H, residual):
+    """eps = 0: a row of zeros gives zeros (scale 0, codes 0); rows whose squares are below float32's range are
+    normalised all the same.  Bounds as in test_gpu_rms_add.py: the sum is at most H / 8 + 8 roundings long
+    there, (H / 32 + 16) in the way tiny rows take, and a subnormal product h w is off by 2^-150, divided by
+    the root mean square like the rest."""
+    r = np.random.RandomState(H)
+    size = 2.0 ** r.randint(-120, 50, (T, 1))
+    size[0] = 2.0 ** -100
+    x = size * r.randn(T, H)
+    res = bf16.from_f64(size * r.randn(T, H)) if residual else None
+    x = bf16.from_f64(x)
+    w = bf16.from_f64(1 + 0.3 * r.randn(H))
+    if T > 2:
+        x[1] = 0
+        if residual:
+            res[1] = 0
+    dres = None if res is None else dev_bf16(res)
+    y, h = api.w4_rms_add(dev_bf16(x), dres, dev_bf16(w), eps=0.0)
+    q, qs, h2 = api.w4_rms_add_q8(dev_bf16(x), dres, dev_bf16(w), eps=0.0)
+    y, q, qs = host_f64(y), q.cpu().numpy().astype(np.float64), qs.cpu().numpy().astype(np.float64)
+    hb = host_bf16_bits(h)
+    assert np.array_equal(hb, host_bf16_bits(h2))
+    zero = ~(hb & 0x7FFF).any(axis=1)
+    assert zero.any() == (T > 2)
+    assert not y[zero].any() and not q[zero].any() and not qs[zero].any()
+    with np.errstate(invalid="ignore"):
+        h_ref, y_ref = decode.rms_add(x, res, w, 0.0)
+    assert np.array_equal(hb, h_ref)
+    y, q, qs, y_ref = (t[~zero] for t in (y, q, qs, y_ref))
+    off = 2.0 ** -150 / np.sqrt(np.mean(bf16.to_f64(h_ref)[~zero] ** 2, axis=1, keepdims=True))
+    rel = (H / 8 + 16) * 2.0 ** -24 * 1.01
+    assert (np.abs(y - y_ref) <= np.abs(y_ref) * (2.0 ** -8 + rel) + 1.01 * off).all()
+    s_ref = np.abs(y_ref).max(axis=1) / 127
+    assert (np.abs(qs - s_ref) <= s_ref * rel + 1.01 * off[:, 0] / 127).all()
+    assert (np.abs(q - y_ref / s_ref[:, None]) <= 0.5 + 127 * 3 * rel + 2 * off / s_ref[:, None]).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-38, 1e-33, 1e-28, 1e-26])
+@pytest.mark.parametrize("T,H", [(5, 256), (4, 2816), (301, 2816), (3, 16392)])
+def test_tiny_rows_beside_a_tiny_eps(eps, T, H):
+    """Rows far below, about and above the root of eps, without a weight, the residual updated in place."""
+    r = np.random.RandomState(T)
+    root = np.sqrt(np.float32(max(eps, 1e-42)).astype(np.float64))
+    size = root * 2.0 ** r.randint(-20, 21, (T, 1))
+    x, res = (bf16.from_f64(size * r.randn(T, H)) for _ in range(2))
+    e = float(np.float32(eps))
+    h_ref, y_ref = decode.rms_add(x, res, None, e)
+    rel = (H / 8 + 16) * 2.0 ** -24 * 1.01
+    buf = dev_bf16(res)
+    y, h = api.w4_rms_add(dev_bf16(x), buf, eps=e, h=buf)
+    assert h is buf and np.array_equal(host_bf16_bits(h), h_ref)
+    assert (np.abs(host_f64(y) - y_ref) <= np.abs(y_ref) * (2.0 ** -8 + rel)).all()
+    buf = dev_bf16(res)
+    q, qs, h = api.w4_rms_add_q8(dev_bf16(x), buf, eps=e, h=buf)
+    assert np.array_equal(host_bf16_bits(h), h_ref)
+    s_ref = np.abs(y_ref).max(axis=1) / 127
+    assert (np.abs(qs.cpu().numpy() - s_ref) <= s_ref * rel).all()
+    assert (np.abs(q.cpu().numpy() - y_ref / s_ref[:, None]) <= 0.5 + 127 * 3 * rel).all()

@@ -76,6 +76,9 @@ struct Args {
   int K, KG;                       // KG = K / 32 groups
   int eights, more;                // few rows: a block's runs of 8 weight rows; the first `more` have one more
   float* parts;                    // [splits][M][N], when K is split over blocks
+  int32_t* dev_status;             // W4_ERR_TIMEOUT where a wait ran out; the sums behind it are NaN
+  uint64_t wait_ns;                // limit of every bounded wait
+  int stall;                       // fault injection for tests: a ring's copies from this stage on are left out
 };
 
 // ------------------------------------------------------------------------------------ few rows
@@ -188,8 +191,10 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
   bool have = at.enter();
   Walk ahead = at;                                     // the next stage to fetch
   bool more = have;
+  int issued = 0, used = 0;                            // stages of this warp's ring
   for (int i = 0; i < S && more; ++i) {
-    if (lane == 0) fetch(ahead, i);
+    if (lane == 0 && issued < a.stall) fetch(ahead, i);
+    ++issued;
     more = ahead.next();
   }
   for (int p0 = warp; p0 < KT * (kUnitGroups / 2); p0 += W * kBatch) {
@@ -234,7 +239,7 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
   for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = 0;
   int st = 0;
   uint32_t parity = 0;                                 // of the ring's current round
-  bool alive = true;                                   // false once a bounded wait ran out: no more waits
+  bool alive = true;                                   // false once a bounded wait ran out: no more waits or copies
   int swz[kUnitGroups];                                // where this lane's word of group g lies in a swizzled row
 #pragma unroll
   for (int g = 0; g < kUnitGroups; ++g) swz[g] = r * 128 + ((g ^ r) << 4) + t * 4;
@@ -245,7 +250,13 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
       const int tile = at.tile, k0 = at.kt, run = min(at.left, KT - k0);
       uint32_t xk = xbase + k0 * (kUnitGroups * 256);
       for (int u = 0; u < run; ++u, xk += kUnitGroups * 256) {
-        if (alive) alive = mbar_wait_ring(&s_full[warp][st], parity);
+        if (alive && !mbar_wait_ring(&s_full[warp][st], parity, a.wait_ns)) {
+          alive = false;
+          set_status(a.dev_status, W4_ERR_TIMEOUT);
+          // A stage that has not arrived is not asked for again, and what is on its way lands before the end.
+          if (lane == 0)
+            for (int i = used; i < min(issued, a.stall); ++i) mbar_wait_ring(&s_full[warp][i % S], (i / S) & 1);
+        }
         const uint32_t base = ring + st * kCodeBytes;
         uint32_t sw[2][4];
         if constexpr (SB == 16) {
@@ -274,8 +285,10 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
           }
         }
         __syncwarp();                                  // the stage has been read
+        ++used;
         if (more) {
-          if (lane == 0) fetch(ahead, st);
+          if (lane == 0 && alive && issued < a.stall) fetch(ahead, st);
+          ++issued;
           more = ahead.next();
         }
         if (++st == S) {
@@ -290,6 +303,7 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
         for (int h = 0; h < 2; ++h) {
           float lo, hi;
           halves(acc[b][h], lo, hi);
+          if (!alive) lo = hi = __int_as_float(0x7FC00000);
           o[(8 * b + 2 * t) * 16 + r + 8 * h] = lo;
           o[(8 * b + 2 * t + 1) * 16 + r + 8 * h] = hi;
           acc[b][h] = 0;
@@ -331,8 +345,6 @@ few_kernel(const __grid_constant__ CUtensorMap codes16, const __grid_constant__ 
     }
     __syncthreads();
   }
-  if (!alive)                                          // copies may still be on their way into this block's memory
-    for (int i = 0; i < S; ++i) mbar_wait_ring(&s_full[warp][i], parity);
 }
 
 // ----------------------------------------------------------------------------------- more rows
@@ -374,9 +386,10 @@ many_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant
   }
   __syncthreads();
 
+  bool alive = true;                                       // false once a bounded wait ran out: no more waits or copies
   auto fetch = [&](int kt, int st) {
     uint8_t* base = smem + st * C::kStage;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && alive && kt - k0 < a.stall) {
       mbar_arrive_expect_tx(s_bar + st, SB == 16 ? C::kStage : C::kScales);
       tma_load_2d(base, &codes_map, kt * 4 * kGS, static_cast<int>(n0), s_bar + st);
       tma_load_2d(base + C::kX, &x_map, kt * 256, static_cast<int>(m0), s_bar + st);
@@ -406,9 +419,14 @@ many_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant
   const uint32_t xb = s0 + C::kX + (wc * C::NT * 8 + tok) * 128 + (t & 1) * 8;
   int st = 0;
   uint32_t parity = 0;
-  bool alive = true;                                       // false once a bounded wait ran out: no more waits
   for (int kt = k0; kt < k1; ++kt) {
-    if (alive) alive = mbar_wait_ring(s_bar + st, parity);
+    if (alive && !mbar_wait_ring(s_bar + st, parity, a.wait_ns)) {
+      alive = false;
+      set_status(a.dev_status, W4_ERR_TIMEOUT);
+      // A stage that has not arrived is not asked for again, and what is on its way lands before the end.
+      if (threadIdx.x == 0)
+        for (int i = kt - k0; i < min(min(kt + C::S - 1, k1) - k0, a.stall); ++i) mbar_wait_ring(s_bar + i % C::S, (i / C::S) & 1);
+    }
     __syncthreads();
     if (kt + C::S - 1 < k1) fetch(kt + C::S - 1, st == 0 ? C::S - 1 : st - 1);
     const uint32_t off = st * C::kStage;
@@ -449,8 +467,6 @@ many_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant
       parity ^= 1;
     }
   }
-  if (!alive)                                              // copies may still be on their way into this block's memory
-    for (int i = 0; i < C::S; ++i) mbar_wait_ring(s_bar + i, parity);
   __syncthreads();
   float* o = reinterpret_cast<float*>(smem);               // [token][kBN + 4]
 #pragma unroll
@@ -461,6 +477,7 @@ many_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant
       for (int h = 0; h < 2; ++h) {
         float lo, hi;
         halves(acc[i][j][h], lo, hi);
+        if (!alive) lo = hi = __int_as_float(0x7FC00000);
         // columns 2 t and 2 t + 1 of the product are these tokens
         const int m = wc * C::NT * 8 + j * 8, n = wr * C::MT * 16 + i * 16 + h * 8 + r;
         o[(m + 4 * (t & 1) + (t >> 1)) * (kBN + 4) + n] = lo;
@@ -633,11 +650,10 @@ size_t w4_linear8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return rows > parts ? rows : parts;
 }
 
-extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
-                                 uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
+static w4_status linear8(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales, uint16_t* y,
+                         int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                         void* stream, uint64_t wait_ns, int stall) {
   using namespace w4;
-  const EntryRange range("w4a8_linear");
   if (M < 0 || N < 1 || K < 32 || K % 32 || N > (1LL << 30) || K > (1LL << 30)) return W4_ERR_INVALID_ARG;
   if (!codes || !scales || !aligned_to(codes, 16) || !aligned_to(scales, 2)) return W4_ERR_INVALID_ARG;
   if (M > 0 && (!xq || !xs || !y)) return W4_ERR_INVALID_ARG;
@@ -647,7 +663,8 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
   if (M == 0) return W4_OK;
   const size_t need = w4_linear8_workspace_bytes(M, N, K);
   if (need && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
-  a8::Args a{xq, xs, codes, scales, y, M, N, static_cast<int>(K), static_cast<int>(K / 32), 0, 0, static_cast<float*>(workspace)};
+  a8::Args a{xq, xs, codes, scales, y, M, N, static_cast<int>(K), static_cast<int>(K / 32), 0, 0, static_cast<float*>(workspace),
+             dev_status, wait_ns, stall};
   auto s = static_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
   // what a copy of consecutive scales may take at once: every row starts at a multiple of it
@@ -669,3 +686,24 @@ extern "C" w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32
                           : BM == 32 ? a8::launch_many<32>(a, splits, SB, sms, s)
                                      : a8::launch_many<64>(a, splits, SB, sms, s));
 }
+
+extern "C" {
+
+w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales, uint16_t* y,
+                      int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  const w4::EntryRange range("w4a8_linear");
+  return linear8(xq, xs, codes, scales, y, M, N, K, workspace, workspace_bytes, nullptr, stream, w4::kWaitLimitNs, 0x7FFFFFFF);
+}
+
+// Fault injection for the tests of the bounded waits (not part of the C ABI in w4a16.h): w4a8_linear with every
+// wait limited to wait_ns and every ring's copies from stage stall_after on left out, so that the waits for them run
+// out.  The kernels then report W4_ERR_TIMEOUT in dev_status and return; nothing faults or hangs.
+w4_status w4_testing_linear8_stall(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
+                                   uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream, uint64_t wait_ns, int32_t stall_after) {
+  const w4::EntryRange range("w4_testing_linear8_stall");
+  if (stall_after < 0) return W4_ERR_INVALID_ARG;
+  return linear8(xq, xs, codes, scales, y, M, N, K, workspace, workspace_bytes, dev_status, stream, wait_ns, stall_after);
+}
+
+}  // extern "C"

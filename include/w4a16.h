@@ -339,6 +339,11 @@ w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint1
 w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
                       uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
                       size_t workspace_bytes, void* stream);
+/* w4a8_linear with a device status: dev_status is one int32 device word or NULL, W4_ERR_TIMEOUT when a bounded
+ * wait inside the kernels ran out (left unchanged otherwise).  Outputs lost to that are NaN, in w4a8_linear too. */
+w4_status w4a8_linear_s(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
+                        uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * kv_cache_write, kv_cache_read -- rows of a paged key/value cache, quantised as they are written and
@@ -428,7 +433,8 @@ typedef enum {
   W4_ENTRY_LINEAR_8 = 3,
   W4_ENTRY_KV_WRITE = 4,
   W4_ENTRY_KV_READ = 5,
-  W4_ENTRY_KV_ATTEND = 6
+  W4_ENTRY_KV_ATTEND = 6,
+  W4_ENTRY_LINEAR_8S = 7
 } w4_entry;
 w4_status w4_packed(int32_t entry, const void* args);
 

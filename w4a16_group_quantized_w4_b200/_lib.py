@@ -42,6 +42,7 @@ W4_ENTRY_LINEAR_8 = 3
 W4_ENTRY_KV_WRITE = 4
 W4_ENTRY_KV_READ = 5
 W4_ENTRY_KV_ATTEND = 6
+W4_ENTRY_LINEAR_8S = 7
 
 # name -> (restype, argtypes), mirroring include/w4a16.h
 _P = C.c_void_p
@@ -64,6 +65,7 @@ SIGNATURES = {
     "w4_rms_add": (_I32, [_P, _P, _P, _I64, _I32, C.c_float, _P, _P, _P]),
     "w4_rms_add_q8": (_I32, [_P, _P, _P, _I64, _I32, C.c_float, _P, _P, _P, _P]),
     "w4a8_linear": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "w4a8_linear_s": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P, _P]),
     "kv_cache_write": (_I32, [_P, _P, _I64, _I64, _P, _I64, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P,
                               _P]),
     "kv_cache_read": (_I32, [_P, _I64, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
@@ -108,7 +110,8 @@ def load(path: str | None = None):
 
 
 _NAMES = {W4_ENTRY_RMS_ADD: "w4_rms_add", W4_ENTRY_RMS_ADD_Q8: "w4_rms_add_q8", W4_ENTRY_LINEAR_8: "w4a8_linear",
-          W4_ENTRY_KV_WRITE: "kv_cache_write", W4_ENTRY_KV_READ: "kv_cache_read", W4_ENTRY_KV_ATTEND: "kv_cache_attend"}
+          W4_ENTRY_KV_WRITE: "kv_cache_write", W4_ENTRY_KV_READ: "kv_cache_read", W4_ENTRY_KV_ATTEND: "kv_cache_attend",
+          W4_ENTRY_LINEAR_8S: "w4a8_linear_s"}
 
 
 def _packer(entry: int):
@@ -130,7 +133,7 @@ def _packer(entry: int):
 
 rms_add = _packer(W4_ENTRY_RMS_ADD)
 rms_add_q8 = _packer(W4_ENTRY_RMS_ADD_Q8)
-linear_8 = _packer(W4_ENTRY_LINEAR_8)
+linear_8 = _packer(W4_ENTRY_LINEAR_8S)
 kv_write = _packer(W4_ENTRY_KV_WRITE)
 kv_read = _packer(W4_ENTRY_KV_READ)
 kv_attend = _packer(W4_ENTRY_KV_ATTEND)

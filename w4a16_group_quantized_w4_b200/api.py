@@ -520,8 +520,9 @@ def w4_rms_add_q8(x, residual=None, weight=None, eps: float = RMS_EPS, h=None, q
 
 
 @_device_call
-def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
-    """y [M, N] = xs * (xq [M, K] int8 @ dequant(codes, scales)^T), bf16 out."""
+def w4a8_linear(xq, xs, codes, scales, y=None, ws=None, dev_status=None):
+    """y [M, N] = xs * (xq [M, K] int8 @ dequant(codes, scales)^T), bf16 out.  dev_status: int32 [1], set where a
+    bounded wait inside the kernels runs out (outputs lost to that are NaN)."""
     if xq.dim() != 2 or codes.dim() != 2:
         raise ValueError("xq, codes: expected two dimensions")
     M, K = xq.shape
@@ -535,9 +536,11 @@ def w4a8_linear(xq, xs, codes, scales, y=None, ws=None):
         y = torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=dev)   # (torch.empty: 0.9 us more)
     else:
         _fits("y", y, torch.bfloat16, (M, N), dev)
+    if dev_status is not None:
+        _fits("dev_status", dev_status, torch.int32, (1,), dev)
     p, n, ws = _scratch(ws, _bytes_needed(_lib.W4_OP_LINEAR_8, M, N, K, 1, dev.index), dev)
     _lib.linear_8(xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K, p, n,
-                  _cur(dev))
+                  _ptr(dev_status), _cur(dev))
     return y
 
 

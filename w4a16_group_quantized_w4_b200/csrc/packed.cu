@@ -52,6 +52,7 @@ extern "C" w4_status w4_packed(int32_t entry, const void* args) {
     case W4_ENTRY_KV_WRITE: return unpack(kv_cache_write, block);
     case W4_ENTRY_KV_READ: return unpack(kv_cache_read, block);
     case W4_ENTRY_KV_ATTEND: return unpack(kv_cache_attend, block);
+    case W4_ENTRY_LINEAR_8S: return unpack(w4a8_linear_s, block);
     default: return W4_ERR_INVALID_ARG;
   }
 }

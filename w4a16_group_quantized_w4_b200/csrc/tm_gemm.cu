@@ -91,6 +91,7 @@ struct Args {
   int32_t* dev_status;
   int tma_out;              // 1: whole 16-token chunks leave through shared memory and TMA stores
   Lay L;
+  int stall;                // EARLY, fault injection for tests: a block's code stages from this one on are left out
 };
 
 // NMAX routed rows per tile, stages of KSK k, TSTAGES token stages, ASLOTS TMEM slots of
@@ -214,7 +215,8 @@ __device__ __forceinline__ void scale_pair(uint32_t s16, float smul, uint32_t& s
 }
 
 
-// EARLY: launched so that it may begin while the conversion runs; it waits where it reads the results.
+// EARLY: launched so that it may begin while the conversion runs; it waits where it reads the results.  It also
+// stores NaN for tiles lost to a wait that ran out (they are left as they were otherwise; both report it).
 template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW, bool EARLY>
 __global__ void __launch_bounds__(32 * (16 + (NSPLIT * KSPLIT - 1) + 4 * (EPIW - 1)), 1)
 tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
@@ -326,6 +328,7 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
         const int32_t row_b = static_cast<int32_t>(wrow(A, T, kBM / 2));
         for (int st = 0; st < nst; ++st) {
           if (!lap0 && !mbar_wait(&cfree[slot], ph)) { ok = false; break; }
+          if (EARLY && issued >= A.stall) continue;
           uint8_t* cdst = smem + L.code + slot * C::kCodeStage;
           mbar_arrive_expect_tx(&cfull[slot], C::kCodeStage);
           tma_load_2d(cdst, &tmap_codes, st * (KSK / 8), row_a, &cfull[slot]);
@@ -468,7 +471,8 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
     int n_out = 0;                                 // TMA stores issued by this warp (lane 0)
     int ti = 0;
     if constexpr (EARLY) pdl_wait();               // the row multipliers
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
+    int t = blockIdx.x;
+    for (; t < total; t += gridDim.x, ++ti) {
       Tile T;
       decode_tile(A, table, offs, t, NMAX, T);
       const int ab = ti % ABUF, hb = ti & 1;
@@ -567,6 +571,14 @@ tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
+    }
+    if constexpr (EARLY) {
+      for (; t < total; t += gridDim.x) {          // only after a wait ran out
+        Tile T;
+        decode_tile(A, table, offs, t, NMAX, T);
+        for (int c0 = 16 * cp; c0 < T.mrows; c0 += 16 * EPIW)
+          for (int tk = c0; tk < min(c0 + 16, T.mrows); ++tk) A.out[(T.r0 + tk) * A.N + T.nt * kBM + l] = 0x7FC0u;
+      }
     }
     if (lane == 0) bulk_wait_all();              // this warp's stores are complete before exit
     __syncwarp();
@@ -818,7 +830,7 @@ static w4_status tm_launch_cfg(const uint32_t* codes, const uint16_t* a16, int64
 
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int early_block);
+                                cudaStream_t stream, int sm_count, int early_block, int stall);
 
 w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int k_div,
                             const uint32_t* codes, const uint16_t* scales, const int32_t* offsets,
@@ -837,15 +849,16 @@ w4_status w4_launch_tm_gemm(const uint16_t* a, const int32_t* a_row_of_pair, int
   w4_launch_a_to_f16(a, a_row_of_pair, kd, a_rows, rows, K, scales, wrows, ws, dev_status, stream,
                      sm_count);
 
-  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count, 0);
+  return w4_launch_tm_prepared(codes, scales, offsets, E, rows, N, K, epi, out, ws, dev_status, stream, sm_count, 0,
+                               0x7FFFFFFF);
 }
 
 // The GEMM on a workspace that the conversion pass has filled (w4_launch_a_to_f16, w4_launch_a8_to_f16).
 // early_block: 192 or 256, the rows of a token block after w4_launch_a8_to_f16, whose kernel lets this one begin
-// while it runs; 0 after the other.
+// while it runs; 0 after the other (stall goes to the early kernels).
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int early_block) {
+                                cudaStream_t stream, int sm_count, int early_block, int stall) {
   w4::tm::Args A{};
   A.rowmul = w4_ws_rowmul(ws, rows, K);
   A.rowexp = w4_ws_rowexp(ws, rows, K);
@@ -854,6 +867,7 @@ w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, c
   A.rows = rows; A.epi = epi; A.out = out;
   A.n_tiles = (epi == W4_EPI_GELU_GATE) ? (N / 2) / (w4::tm::kBM / 2) : N / w4::tm::kBM;
   A.dev_status = dev_status;
+  A.stall = stall;
   const uint16_t* a16 = w4_ws_a16(ws);
   if (early_block == 256)
     return tm_launch_cfg<256, 128, 5, 4, 1, 1, 1, 2, true>(codes, a16, rows, K, A, stream, sm_count);

@@ -26,7 +26,7 @@
 bool w4_tm_supported(int N, int K, int epi);
 w4_status w4_launch_tm_prepared(const uint32_t* codes, const uint16_t* scales, const int32_t* offsets, int E,
                                 int64_t rows, int N, int K, int epi, uint16_t* out, void* ws, int32_t* dev_status,
-                                cudaStream_t stream, int sm_count, int early_block);
+                                cudaStream_t stream, int sm_count, int early_block, int stall);
 
 namespace w4 {
 namespace a8 {
@@ -678,7 +678,7 @@ static w4_status linear8(const int8_t* xq, const float* xs, const uint32_t* code
     w4_launch_a8_to_f16(xq, xs, M, static_cast<int>(K), scales, N, workspace, s);
     if (cudaGetLastError() != cudaSuccess) return w4_record_status(W4_ERR_CUDA);
     return w4_record_status(w4_launch_tm_prepared(codes, scales, nullptr, 1, M, static_cast<int>(N), static_cast<int>(K),
-                                                  W4_EPI_NONE, y, workspace, nullptr, s, sms, block));
+                                                  W4_EPI_NONE, y, workspace, dev_status, s, sms, block, stall));
   }
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);
@@ -695,8 +695,15 @@ w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, 
   return linear8(xq, xs, codes, scales, y, M, N, K, workspace, workspace_bytes, nullptr, stream, w4::kWaitLimitNs, 0x7FFFFFFF);
 }
 
+w4_status w4a8_linear_s(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales, uint16_t* y,
+                        int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        void* stream) {
+  const w4::EntryRange range("w4a8_linear_s");
+  return linear8(xq, xs, codes, scales, y, M, N, K, workspace, workspace_bytes, dev_status, stream, w4::kWaitLimitNs, 0x7FFFFFFF);
+}
+
 // Fault injection for the tests of the bounded waits (not part of the C ABI in w4a16.h): w4a8_linear with every
-// wait limited to wait_ns and every ring's copies from stage stall_after on left out, so that the waits for them run
+// wait limited to wait_ns (the tensor-memory kernel's to kWaitLimitNs as always: a limit of the call's own cost 2%) and every ring's copies from stage stall_after on left out, so that the waits for them run
 // out.  The kernels then report W4_ERR_TIMEOUT in dev_status and return; nothing faults or hangs.
 w4_status w4_testing_linear8_stall(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
                                    uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,

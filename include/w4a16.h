@@ -329,12 +329,13 @@ w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint1
  *   M >= 0, N >= 1, K >= 32 with K % 32 == 0.
  *   workspace at least w4_workspace_bytes(W4_OP_LINEAR_8, M, N, K, 1, 1) bytes (may be NULL when that
  *             is 0).  Its contents need no preparation; calls sharing it must not overlap on the GPU.
- * Up to 32 rows, and for shapes that the tensor-memory kernel of w4a16_linear does not take, sums
+ * Up to 32 rows that fit in shared memory (K <= 23040 up to 8 rows, 11008 up to 16, 4864 up to 32) go to a kernel of
+ * their own.  There, and for shapes that the tensor-memory kernel of w4a16_linear does not take, sums
  * inside a group are exact integers and groups are accumulated in float32 in a fixed order.  More rows
  * of shapes that it takes (N % 128 == 0, K % 64 == 0, K <= 4096, scales 4-byte aligned) go to that kernel
  * where it is the faster one: every product is exact (of scales within 2^21 of their row's largest; smaller
  * ones keep fewer bits), the sums are float32.  Either way a call gives the same bits every time.
- * N <= 8388480 for more than 32 rows (W4_ERR_UNSUPPORTED beyond).
+ * N <= 8388480 for calls that go to neither of the two (W4_ERR_UNSUPPORTED beyond).
  */
 w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,
                       uint16_t* y, int64_t M, int64_t N, int64_t K, void* workspace,

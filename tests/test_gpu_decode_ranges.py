@@ -12,7 +12,8 @@ import torch
 from oracle import bf16, decode
 from w4a16_group_quantized_w4_b200 import api
 from tests._util import dev_bf16, host_bf16_bits, host_f64
-from tests.test_gpu_kv_cache import KINDS, host_codes, stored
+from tests.test_gpu_kv_cache import KINDS
+from tests.test_gpu_rms_add import check_linear, linear_case
 
 pytestmark = pytest.mark.gpu
 
@@ -279,3 +280,9 @@ def test_tiny_rows_beside_a_tiny_eps(eps, T, H):
     s_ref = np.abs(y_ref).max(axis=1) / 127
     assert (np.abs(qs.cpu().numpy() - s_ref) <= s_ref * rel).all()
     assert (np.abs(q.cpu().numpy() - y_ref / s_ref[:, None]) <= 0.5 + 127 * 3 * rel).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 300, 8192), (32, 1024, 5120), (31, 129, 32 * 161), (17, 19000, 4928), (20, 5, 4896)])
+def test_linear_of_17_to_32_rows_too_long_for_shared_memory(M, N, K):
+    """The tiled kernel with 32 tokens a tile: K split and whole, scales by TMA and not."""
+    check_linear(*linear_case(M, N, K, M + N))

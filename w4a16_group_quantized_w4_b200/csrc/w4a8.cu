@@ -626,7 +626,6 @@ w4_status launch_many(const Args& a, int splits, int SB, int sms, cudaStream_t s
   else if (!encode(&scales, a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.N, a.KG, kGS, kBN, CU_TENSOR_MAP_SWIZZLE_NONE))
     return W4_ERR_CUDA;
   const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + kBN - 1) / kBN;
-  if (tm > 0x7FFFFFFFLL || tn > 65535) return W4_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(tm), static_cast<unsigned>(tn), splits);
   kernel<<<grid, 256, Many<BM>::kSmem, s>>>(codes, scales, x, a);
   if (cudaGetLastError() != cudaSuccess) return W4_ERR_CUDA;
@@ -680,6 +679,7 @@ static w4_status linear8(const int8_t* xq, const float* xs, const uint32_t* code
     return w4_record_status(w4_launch_tm_prepared(codes, scales, nullptr, 1, M, static_cast<int>(N), static_cast<int>(K),
                                                   W4_EPI_NONE, y, workspace, dev_status, s, sms, block, stall));
   }
+  if (N > 65535LL * a8::kBN) return W4_ERR_UNSUPPORTED;       // (a grid's y)
   const int splits = a8::many_splits(M, N, K / 32, sms);
   const int BM = a8::many_tile(M);
   return w4_record_status(BM == 16 ? a8::launch_many<16>(a, splits, SB, sms, s)

@@ -650,7 +650,8 @@ def kv_cache_attend(q, k_cache, v_cache, page_table, seq_lens, k_scales=None, v_
 
 class KVCache:
     """One layer's paged key/value cache and the calls on it.  kind: "bf16", "int8" or "int4" (codes
-    with one bf16 scale per 32 elements of head_dim).  Freshly made it is zero throughout."""
+    with one bf16 scale per 32 elements of head_dim).  Freshly made it is zero throughout.  Rows of every head_dim that
+    is a multiple of 32, up to 1024, are written and read; attention takes 64, 128, 192 and 256."""
 
     def __init__(self, pages: int, kv_heads: int, page_size: int, head_dim: int, kind: str = "int8", device="cuda"):
         if kind not in ("bf16", "int8", "int4"):

@@ -50,6 +50,8 @@ class AttentionBlock:
                  norm_in=None, norm_out=None, softcap: float = 0.0, window: int = 0):
         _, kv_heads, _, last = cache.k.shape
         self.dim = last * (8 if cache.kind == "int4" else 1)
+        if self.dim not in (64, 128, 192, 256):
+            raise ValueError(f"cache: attention takes a head_dim of 64, 128, 192 or 256, got {self.dim}")
         self.q_heads, self.kv_heads = q_heads, kv_heads
         if qkv_codes.shape[0] != (q_heads + 2 * kv_heads) * self.dim:
             raise ValueError("qkv_codes: rows must be (q_heads + 2 kv_heads) * head_dim")

@@ -43,11 +43,13 @@ class AttentionBlock:
       a = attention of q over the cache;  o = a Wo^T;  h <- h + o;  returns norm(h) for the expert layer.
 
     qkv_codes [(q_heads + 2 kv_heads) D, H/8] with scales [.., H/32], o_codes [H, q_heads D / 8] with
-    scales [.., q_heads D / 32] (layout L1); norms: two bf16 [H] weights or None.  Queries and keys
-    are taken as the projection gives them."""
+    scales [.., q_heads D / 32] (layout L1); norms: two bf16 [H] weights or None, with one eps.  Queries and
+    keys are taken as the projection gives them; scale: what their products are multiplied by, 1 / sqrt(D) when
+    None.  D, the cache's head_dim: one that attention takes (64, 128, 192 or 256)."""
 
     def __init__(self, qkv_codes, qkv_scales, o_codes, o_scales, cache: api.KVCache, q_heads: int,
-                 norm_in=None, norm_out=None, softcap: float = 0.0, window: int = 0):
+                 norm_in=None, norm_out=None, softcap: float = 0.0, window: int = 0, scale: float | None = None,
+                 eps: float = api.RMS_EPS):
         _, kv_heads, _, last = cache.k.shape
         self.dim = last * (8 if cache.kind == "int4" else 1)
         if self.dim not in (64, 128, 192, 256):
@@ -59,21 +61,23 @@ class AttentionBlock:
             raise ValueError("o_codes: columns must be q_heads * head_dim / 8")
         self.qkv, self.o = (qkv_codes, qkv_scales), (o_codes, o_scales)
         self.cache, self.norm_in, self.norm_out = cache, norm_in, norm_out
-        self.softcap, self.window = softcap, window
+        self.softcap, self.window, self.scale, self.eps = softcap, window, scale, eps
 
-    def __call__(self, x, h, page_table, seq_lens, slots, stream=None):
+    def __call__(self, x, h, page_table, seq_lens, slots, stream=None, dev_status=None):
         """x bf16 [T, H] (the previous layer's output), h bf16 [T, H] the residual stream or None for
         the first layer; page_table, seq_lens as in kv_cache_attend (the new token counted), slots
-        int64 [T] of the new rows -> (the expert layer's input, h)."""
+        int64 [T] of the new rows -> (the expert layer's input, h).  dev_status: int32 [1] that the 8-bit linear, the
+        write and the attention report to (a slot past the cache, a length or page out of range)."""
         with _placed(x, stream):
             T = x.shape[0]
-            n, ns, h = api.w4_rms_add_q8(x, h, self.norm_in)
-            rows = api.w4a8_linear(n, ns, *self.qkv).unflatten(1, (-1, self.dim))
+            n, ns, h = api.w4_rms_add_q8(x, h, self.norm_in, eps=self.eps)
+            rows = api.w4a8_linear(n, ns, *self.qkv, dev_status=dev_status).unflatten(1, (-1, self.dim))
             q, k, v = rows.split((self.q_heads, self.kv_heads, self.kv_heads), dim=1)
-            self.cache.write(k, v, slots)
-            a = self.cache.attend(q, page_table, seq_lens, softcap=self.softcap, window=self.window)
+            self.cache.write(k, v, slots, dev_status=dev_status)
+            a = self.cache.attend(q, page_table, seq_lens, scale=self.scale, softcap=self.softcap, window=self.window,
+                                  dev_status=dev_status)
             o = api.w4a16_linear(a.view(T, -1), *self.o, ws=api.linear_scratch(T, *self.o[0].shape, x.device))
-            return api.w4_rms_add(o, h, self.norm_out)
+            return api.w4_rms_add(o, h, self.norm_out, eps=self.eps)
 
 
 class MoEStack:
@@ -152,12 +156,12 @@ class MoEStack:
         return xs, ys
 
     def decode_step(self, x0, logits, blocks, page_table, seq_lens, slots, norm=None, stream=None,
-                    fused: bool = False):
+                    fused: bool = False, dev_status=None, eps: float = api.RMS_EPS):
         """One decode step through attention and experts: layer l runs blocks[l] (AttentionBlock, each
         with its own cache; they share page_table, seq_lens and slots) and expert layer l on
         logits[l] f32 [T, E], around the residual stream that x0 bf16 [T, H] begins.  Returns
-        (norm of the final residual stream with weight `norm`, the stream), both bf16 [T, H].  Rows whose
-        slot is negative and whose length is 0 are padding.  The expert layers share scratch and keep their
+        (norm of the final residual stream with weight `norm` and eps, the stream), both bf16 [T, H].  Rows whose
+        slot is negative and whose length is 0 are padding.  dev_status: int32 [1] that the blocks report to.  The expert layers share scratch and keep their
         buffers (allocated by the first step of a T and path: run one before capturing one): two steps must
         not overlap on the GPU, nor two captured ones be replayed at once."""
         if len(blocks) != self.L:
@@ -166,9 +170,9 @@ class MoEStack:
         with _placed(x0, stream):
             y, h = x0, None
             for l, block in enumerate(blocks):
-                x, h = block(y, h, page_table, seq_lens, slots)
+                x, h = block(y, h, page_table, seq_lens, slots, dev_status=dev_status)
                 y = self.layer(l, T, fused)(x, logits[l])
-            return api.w4_rms_add(y, h, norm)
+            return api.w4_rms_add(y, h, norm, eps=eps)
 
     def expert_bytes(self) -> int:
         """Packed bytes of one expert (gate/up + down codes and scales)."""

@@ -334,7 +334,8 @@ w4_status w4_rms_add_q8(const uint16_t* x, const uint16_t* residual, const uint1
  * inside a group are exact integers and groups are accumulated in float32 in a fixed order.  More rows
  * of shapes that it takes (N % 128 == 0, K % 64 == 0, K <= 4096, scales 4-byte aligned) go to that kernel
  * where it is the faster one: every product is exact (of scales within 2^21 of their row's largest; smaller
- * ones keep fewer bits), the sums are float32.  Either way a call gives the same bits every time.
+ * ones keep fewer bits), the sums are float32, and |xs| has to stay below 2^92 (2^35 is multiplied by it in
+ * front of the last power of two).  Either way a call gives the same bits every time.
  * N <= 8388480 for calls that go to neither of the two (W4_ERR_UNSUPPORTED beyond).
  */
 w4_status w4a8_linear(const int8_t* xq, const float* xs, const uint32_t* codes, const uint16_t* scales,

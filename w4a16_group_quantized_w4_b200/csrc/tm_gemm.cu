@@ -215,8 +215,9 @@ __device__ __forceinline__ void scale_pair(uint32_t s16, float smul, uint32_t& s
 }
 
 
-// EARLY: launched so that it may begin while the conversion runs; it waits where it reads the results.  It also
-// stores NaN for tiles lost to a wait that ran out (they are left as they were otherwise; both report it).
+// EARLY: launched so that it may begin while the conversion runs; it waits where it reads the results.  Codes and
+// scales it reads before that: the conversion does not write them, and as it was launched the ordinary way, whatever
+// wrote them in front of it is complete.  It also stores NaN for tiles lost to a wait that ran out (they are left as they were otherwise; both report it).
 template <int NMAX, int KSK, int TSTAGES, int ASLOTS, int NSPLIT, int KSPLIT, int ABUF, int EPIW, bool EARLY>
 __global__ void __launch_bounds__(32 * (16 + (NSPLIT * KSPLIT - 1) + 4 * (EPIW - 1)), 1)
 tm_gemm_kernel(const __grid_constant__ CUtensorMap tmap_codes,
